@@ -226,6 +226,104 @@ dg_status dg_quantize_fp8_128x128(const void *X, int x_dtype, uint8_t *Q, float 
 dg_status dg_transpose_fp8(const uint8_t *X, uint8_t *Y, int64_t rows, int64_t cols,
                            void *stream);
 
+/* ---------------------------------------------------------------------------------
+ * The gate of a mixture of experts: from a row's logits to the experts that the grouped
+ * calls above compute for it, and what training needs of that choice.
+ *
+ * For each row t of the T x E logits z (row-major, DEVICE, row stride ld >= E elements,
+ * dtype DG_IN_F32 or DG_IN_BF16), in fp32:
+ *   scores   s_te = softmax over e (DG_SCORE_SOFTMAX) or sigmoid of z_te (DG_SCORE_SIGMOID)
+ *   choice   ids[t][0..k) = the experts of the k largest keys z_te + bias_e (one fp32
+ *            addition; bias NULL: z_te), in decreasing order, equal keys in increasing order
+ *            of e.  A key of -inf or NaN is never chosen: a bias of -inf closes an expert;
+ *            choices that are left without an expert have id -1 and weight 0.
+ *   weights  weights[t][j] = scale * s of the choice, divided, if `normalize` is non-zero,
+ *            by the sum of the row's chosen scores (0 where that sum is 0).  The bias is
+ *            part of the choice only.
+ *   row_valid (T bytes or NULL: all rows): a row of 0 is padding.  Its logits are not read;
+ *            its ids are -1, its weights 0, and it is in no count, loss or gradient.
+ * and over the rows:
+ *   counts   counts[e] = choices of expert e (the masked call's masked_m, or the contiguous
+ *            call's segment lengths before their alignment)
+ *   loss     balance * sum_e f_e P_e, f_e = E counts[e] / (k V), P_e = the mean over the V
+ *            valid rows of p_te, with p = s (softmax) or s / sum_e s (sigmoid); 0 if V = 0.
+ *            Its derivative by p_te, f being a constant, is the same for every valid row:
+ *   coef     coef[e] = balance * f_e / V, what the backward pass needs of the loss.
+ * A row of -inf only has no choice and no probabilities; a row with a NaN, or under softmax
+ * with a +inf, has NaN weights and makes the loss NaN (ids stay in range).
+ *
+ * 1 <= E <= 1024, 1 <= k <= min(E, 16), T >= 0 (T = 0: counts, loss and coef are written as
+ * zeros, nothing else).  counts may be NULL; loss and coef are both given or both NULL, and
+ * need counts.  Pointers need their element's alignment only (rows that start on 16 bytes,
+ * 8 for bf16, with E and ld multiples of 4, are read in wider loads).
+ *
+ * With counts the call needs a workspace of dg_moe_route_workspace_bytes bytes, 16-byte
+ * aligned, whose first 256 bytes are zero before its first use and are left zero by every
+ * call; the rest may hold anything.  It can serve this call and dg_lora_bf16 in stream
+ * order, not two calls that may overlap, and not the GEMM calls, which need all of theirs
+ * zero.
+ *
+ * Sums over rows are taken in an order that depends on the sizes only: the same inputs give
+ * the same bits.
+ * Errors, in this order: DG_ERR_SHAPE, DG_ERR_FORMAT (dtype or score), DG_ERR_NULL,
+ * DG_ERR_ALIGN, DG_ERR_WORKSPACE, DG_ERR_DEVICE, DG_ERR_HIP.  Asynchronous on `stream`,
+ * no readback, graph-capturable. */
+#define DG_SCORE_SOFTMAX 0
+#define DG_SCORE_SIGMOID 1
+
+size_t dg_moe_route_workspace_bytes(int64_t T, int64_t E);
+dg_status dg_moe_route(const void *logits, int dtype, int64_t ld, const float *bias,
+                       const uint8_t *row_valid, int64_t T, int64_t E, int64_t k, int score,
+                       int normalize, float scale, float balance, int32_t *ids,
+                       float *weights, int32_t *counts, float *loss, float *coef,
+                       void *workspace, size_t workspace_bytes, void *stream);
+
+/* Backward pass of dg_moe_route: grad_logits (T x E, row stride ld_grad, dtype of the
+ * logits; every element is written, padding rows with zeros) = the gradient by the logits of
+ *   sum_tj grad_weights[t][j] weights[t][j] + grad_loss * loss
+ * with the choice and the counts held constant.  logits, row_valid, score, normalize, scale
+ * as in the forward call, ids and coef its outputs.  grad_weights NULL: no first term (ids
+ * may then be NULL).  coef NULL: no second term; grad_loss (one fp32 in DEVICE memory) NULL
+ * with coef: 1.  ids outside [0, E) are skipped; a row's ids must differ from each other.
+ * No workspace.  Errors and execution as above. */
+dg_status dg_moe_route_backward(const void *logits, int dtype, int64_t ld,
+                                const uint8_t *row_valid, int64_t T, int64_t E, int64_t k,
+                                int score, int normalize, float scale, const int32_t *ids,
+                                const float *grad_weights, const float *coef,
+                                const float *grad_loss, void *grad_logits, int64_t ld_grad,
+                                void *stream);
+
+/* ---------------------------------------------------------------------------------
+ * Low-rank adapters of many requests beside a shared projection (dg_gemm_fp8_nt's output,
+ * or any other bf16 matrix, as `base`):
+ *
+ *   out[t,n] = bf16( base[t,n] + scales[i] * sum_r ( sum_k X[t,k] A_i[r,k] ) B_i[n,r] )
+ *
+ * with i = ids[t], r < ranks[i].  Rows whose id is outside [0, L) have no adapter: out =
+ * base.  All DEVICE, row-major:
+ *   X  bf16, T x K, row stride ldx     A  bf16, L x R x K     B  bf16, L x N x R
+ *   ids int32, T   scales fp32, L (NULL: 1)   ranks int32, L (NULL: all R; clamped to
+ *   [0, R] on the device; what A and B hold past an adapter's rank does not count)
+ *   base bf16, T x N, row stride ld_base (NULL: zero; may be `out` itself with the same
+ *   stride, not overlap it otherwise)         out bf16, T x N, row stride ld_out
+ * Rows of one adapter may be anywhere.  A row's result depends on its own adapter's values
+ * only, whatever other adapters hold.  Sums are fp32; the inner product is kept to 16
+ * significant bits or more and the result rounded once, to nearest even.
+ *
+ * T, N >= 0 (0: nothing to do), K > 0 and K % 128 == 0, K <= 2^22, 8 <= R <= 128 and
+ * R % 8 == 0, L >= 1, ldx % 8 == 0, strides at least the row's length (DG_ERR_SHAPE).
+ * X, A, B 16-byte aligned, base and out 2-byte (faster: 16-byte with strides that 8
+ * divides).  Workspace: dg_lora_workspace_bytes bytes, 16-byte aligned; the first 256 bytes
+ * are not touched (see dg_moe_route), the rest may hold anything before and after.
+ * Errors, in this order: DG_ERR_SHAPE, DG_ERR_NULL, DG_ERR_ALIGN, DG_ERR_WORKSPACE,
+ * DG_ERR_DEVICE, DG_ERR_HIP.  Asynchronous on `stream`, graph-capturable, deterministic. */
+size_t dg_lora_workspace_bytes(int64_t T, int64_t N, int64_t K, int64_t R, int64_t L);
+dg_status dg_lora_bf16(const uint16_t *X, int64_t ldx, const uint16_t *A, const uint16_t *B,
+                       const int32_t *ids, const float *scales, const int32_t *ranks,
+                       const uint16_t *base, int64_t ld_base, uint16_t *out, int64_t ld_out,
+                       int64_t T, int64_t N, int64_t K, int64_t R, int64_t L,
+                       void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

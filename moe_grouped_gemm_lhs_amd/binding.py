@@ -76,6 +76,20 @@ def load_library():
         lib.dg_grouped_gemm_fp8_masked_ex.restype = I
         lib.dg_grouped_gemm_fp8_masked_ex.argtypes = [P, I, P, P, I, P, P, P, I64, I64, I64,
                                                       I64, P, SZ, P]
+        F = ctypes.c_float
+        lib.dg_moe_route_workspace_bytes.restype = SZ
+        lib.dg_moe_route_workspace_bytes.argtypes = [I64, I64]
+        lib.dg_moe_route.restype = I
+        lib.dg_moe_route.argtypes = [P, I, I64, P, P, I64, I64, I64, I, I, F, F, P, P, P, P, P, P,
+                                     SZ, P]
+        lib.dg_moe_route_backward.restype = I
+        lib.dg_moe_route_backward.argtypes = [P, I, I64, P, I64, I64, I64, I, I, F, P, P, P, P, P,
+                                              I64, P]
+        lib.dg_lora_workspace_bytes.restype = SZ
+        lib.dg_lora_workspace_bytes.argtypes = [I64, I64, I64, I64, I64]
+        lib.dg_lora_bf16.restype = I
+        lib.dg_lora_bf16.argtypes = [P, I64, P, P, P, P, P, P, I64, P, I64, I64, I64, I64, I64, I64,
+                                     P, SZ, P]
         _lib = lib
     return _lib
 

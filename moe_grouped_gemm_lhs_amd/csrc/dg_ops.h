@@ -1,0 +1,74 @@
+// dg_ops.h -- shared between the host side of the gate and the adapters (dg_ops_host.cpp)
+// and their kernels (dg_route.hip, dg_lora.hip).  Not part of the public ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace dg {
+
+// The first bytes of the operators' workspace: the arrival counter
+// of the gate's workgroups, zero between calls.  What a call keeps for itself follows.
+constexpr int kRouteWsHeader = 256;
+
+// The gate and its backward pass (defined in dg_route.hip).
+constexpr int kRouteMaxK = 16;       // choices a row
+constexpr int kRouteMaxE = 1024;     // experts
+constexpr int kRouteMaxGrid = 512;   // workgroups
+
+struct RouteArgs {
+  const void* logits;
+  int64_t ld;                  // row stride of the logits
+  const float* bias;           // E, or nullptr
+  const uint8_t* row_valid;    // T, or nullptr
+  int64_t T;
+  int E, k;
+  int bf16, sigmoid, normalize, vec;   // vec: rows may be read four logits at a time
+  float scale, balance;
+  // forward
+  int32_t* ids;
+  float* weights;
+  int32_t* counts;             // or nullptr
+  float* loss;                 // or nullptr
+  float* coef;                 // with loss; read in the backward pass (or nullptr)
+  void* workspace;
+  // backward
+  const int32_t* ids_in;
+  const float* grad_weights;   // or nullptr
+  const float* grad_loss;      // or nullptr (1)
+  void* grad_logits;
+  int64_t ld_grad;
+  int vec_grad;
+};
+
+int route_grid(int64_t T, int64_t E);
+void launch_route(const RouteArgs& a, bool backward, int grid, hipStream_t stream);
+
+// Low-rank adapters (defined in dg_lora.hip).
+constexpr int kLoraMaxR = 128;
+constexpr int kLoraDownFrags = 16;   // 32-deep pieces of K in a wave's registers
+
+struct LoraArgs {
+  const uint16_t* x;
+  int64_t ldx;
+  const uint16_t* A;
+  const uint16_t* B;
+  const int32_t* ids;
+  const float* scales;         // L, or nullptr (1)
+  const int32_t* ranks;        // L, or nullptr (R)
+  const uint16_t* base;        // or nullptr (0); may be out
+  int64_t ld_base;
+  uint16_t* out;
+  int64_t ld_out;
+  float* h;                    // S x T x R, in the workspace
+  int64_t T, N;
+  int K, R, L;
+  int S, Q;                    // shares of K, workgroups that share a tile's adapters
+};
+
+// Shares of K and workgroups over a tile's adapters for these sizes.
+void lora_split(int64_t T, int64_t K, int64_t R, int* S, int* Q);
+void launch_lora(const LoraArgs& a, hipStream_t stream);
+
+}  // namespace dg
