@@ -240,8 +240,8 @@ dg_status dg_transpose_fp8(const uint8_t *X, uint8_t *Y, int64_t rows, int64_t c
  *   weights  weights[t][j] = scale * s of the choice, divided, if `normalize` is non-zero,
  *            by the sum of the row's chosen scores (0 where that sum is 0).  The bias is
  *            part of the choice only.
- *   row_valid (T bytes or NULL: all rows): a row of 0 is padding.  Its logits are not read;
- *            its ids are -1, its weights 0, and it is in no count, loss or gradient.
+ *   row_valid (T bytes or NULL: all rows): a row of 0 is padding.  Its logits may be
+ *            anything; its ids are -1, its weights 0, and it is in no count, loss or gradient.
  * and over the rows:
  *   counts   counts[e] = choices of expert e (the masked call's masked_m, or the contiguous
  *            call's segment lengths before their alignment)
@@ -258,10 +258,9 @@ dg_status dg_transpose_fp8(const uint8_t *X, uint8_t *Y, int64_t rows, int64_t c
  * 8 for bf16, with E and ld multiples of 4, are read in wider loads).
  *
  * With counts the call needs a workspace of dg_moe_route_workspace_bytes bytes, 16-byte
- * aligned, whose first 256 bytes are zero before its first use and are left zero by every
- * call; the rest may hold anything.  It can serve this call and dg_lora_bf16 in stream
- * order, not two calls that may overlap, and not the GEMM calls, which need all of theirs
- * zero.
+ * aligned.  It may hold anything before and after the call, so one buffer can serve this
+ * call and dg_lora_bf16 in stream order (not two calls that may overlap, and not the GEMM
+ * calls, which need theirs zero).
  *
  * Sums over rows are taken in an order that depends on the sizes only: the same inputs give
  * the same bits.
@@ -313,8 +312,8 @@ dg_status dg_moe_route_backward(const void *logits, int dtype, int64_t ld,
  * T, N >= 0 (0: nothing to do), K > 0 and K % 128 == 0, K <= 2^22, 8 <= R <= 128 and
  * R % 8 == 0, L >= 1, ldx % 8 == 0, strides at least the row's length (DG_ERR_SHAPE).
  * X, A, B 16-byte aligned, base and out 2-byte (faster: 16-byte with strides that 8
- * divides).  Workspace: dg_lora_workspace_bytes bytes, 16-byte aligned; the first 256 bytes
- * are not touched (see dg_moe_route), the rest may hold anything before and after.
+ * divides).  Workspace: dg_lora_workspace_bytes bytes, 16-byte aligned; it may hold
+ * anything before and after (see dg_moe_route).
  * Errors, in this order: DG_ERR_SHAPE, DG_ERR_NULL, DG_ERR_ALIGN, DG_ERR_WORKSPACE,
  * DG_ERR_DEVICE, DG_ERR_HIP.  Asynchronous on `stream`, graph-capturable, deterministic. */
 size_t dg_lora_workspace_bytes(int64_t T, int64_t N, int64_t K, int64_t R, int64_t L);

@@ -8,14 +8,14 @@
 
 namespace dg {
 
-// The first bytes of the operators' workspace: the arrival counter
-// of the gate's workgroups, zero between calls.  What a call keeps for itself follows.
-constexpr int kRouteWsHeader = 256;
+// First bytes of the gate's workspace, before its workgroups' sums.
+constexpr int kRouteWsHeader = 512;
 
 // The gate and its backward pass (defined in dg_route.hip).
 constexpr int kRouteMaxK = 16;       // choices a row
 constexpr int kRouteMaxE = 1024;     // experts
 constexpr int kRouteMaxGrid = 512;   // workgroups
+constexpr int64_t kRouteWideWork = (int64_t)1 << 21;   // logits from which V = 32
 
 struct RouteArgs {
   const void* logits;
@@ -42,8 +42,11 @@ struct RouteArgs {
   int vec_grad;
 };
 
-int route_grid(int64_t T, int64_t E);
-void launch_route(const RouteArgs& a, bool backward, int grid, hipStream_t stream);
+// Workgroups' sums (of E probabilities, E counts and the rows) that the forward pass keeps in
+// the workspace for these sizes.
+int route_slots(int64_t T, int64_t E);
+void launch_route(const RouteArgs& a, hipStream_t stream);
+void launch_route_backward(const RouteArgs& a, hipStream_t stream);
 
 // Low-rank adapters (defined in dg_lora.hip).
 constexpr int kLoraMaxR = 128;

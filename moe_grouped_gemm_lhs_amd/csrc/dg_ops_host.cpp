@@ -65,7 +65,7 @@ extern "C" {
 
 size_t dg_moe_route_workspace_bytes(int64_t T, int64_t E) {
   if (!route_shape(T, E, 1, E)) return 0;
-  return dg::kRouteWsHeader + (size_t)dg::route_grid(T, E) * (8 * (size_t)E + 4);
+  return dg::kRouteWsHeader + (size_t)dg::route_slots(T, E) * (8 * (size_t)E + 4);
 }
 
 dg_status dg_moe_route(const void* logits, int dtype, int64_t ld, const float* bias,
@@ -94,7 +94,7 @@ dg_status dg_moe_route(const void* logits, int dtype, int64_t ld, const float* b
   a.scale = scale; a.balance = balance; a.ids = ids; a.weights = weights; a.counts = counts;
   a.loss = loss; a.coef = coef; a.workspace = workspace;
   (void)hipGetLastError();
-  dg::launch_route(a, false, dg::route_grid(T, E), (hipStream_t)stream);
+  dg::launch_route(a, (hipStream_t)stream);
   return hipGetLastError() == hipSuccess ? DG_OK : DG_ERR_HIP;
 }
 
@@ -121,7 +121,7 @@ dg_status dg_moe_route_backward(const void* logits, int dtype, int64_t ld, const
   a.grad_logits = grad_logits; a.ld_grad = ld_grad;
   a.vec_grad = route_vec(grad_logits, E, ld_grad, bf16);
   (void)hipGetLastError();
-  dg::launch_route(a, true, dg::route_grid(T, E), (hipStream_t)stream);
+  dg::launch_route_backward(a, (hipStream_t)stream);
   return hipGetLastError() == hipSuccess ? DG_OK : DG_ERR_HIP;
 }
 
@@ -129,7 +129,7 @@ size_t dg_lora_workspace_bytes(int64_t T, int64_t N, int64_t K, int64_t R, int64
   if (!lora_shape(T, N, K, R, L) || T == 0 || N == 0) return 0;
   int S = 0, Q = 0;
   dg::lora_split(T, K, R, &S, &Q);
-  return dg::kRouteWsHeader + (size_t)S * T * R * 4;
+  return (size_t)S * T * R * 4;
 }
 
 dg_status dg_lora_bf16(const uint16_t* X, int64_t ldx, const uint16_t* A, const uint16_t* B,
@@ -155,7 +155,7 @@ dg_status dg_lora_bf16(const uint16_t* X, int64_t ldx, const uint16_t* A, const 
   dg::LoraArgs a{};
   a.x = X; a.ldx = ldx; a.A = A; a.B = B; a.ids = ids; a.scales = scales; a.ranks = ranks;
   a.base = base; a.ld_base = ld_base; a.out = out; a.ld_out = ld_out;
-  a.h = (float*)((uint8_t*)workspace + dg::kRouteWsHeader);
+  a.h = (float*)workspace;
   a.T = T; a.N = N; a.K = (int)K; a.R = (int)R; a.L = (int)L;
   dg::lora_split(T, K, R, &a.S, &a.Q);
   (void)hipGetLastError();

@@ -7,10 +7,14 @@
 // of lane l, so that a chunk c is one 16-byte (fp32) or 8-byte (bf16) load a lane and
 // consecutive lanes read consecutive addresses.
 //
-// Choice of experts.  The key fp32(z + bias) is widened to a double, whose low 29 mantissa
-// bits are then zero, and the expert's index goes into the lowest ten of them, so that of
-// two equal keys the lower index is the larger double.  All keys of a row differ, and one
-// maximum finds both the largest key and, among equals, the lowest expert.
+// Choice of experts.  A key fp32(z + bias) becomes a double whose high word is the key's
+// bits and whose low word says the expert: both formats order by sign, then magnitude, so
+// doubles made this way compare as the keys do (an fp32 infinity is an ordinary double),
+// and between equal keys the low word decides, in favour of the lower expert.  No two of a
+// row are equal, so one v_max_f64 / v_min_f64 pair orders two candidates completely: each
+// lane sorts its candidates by blocks, keeps the best KM >= k, and the lanes' lists are
+// merged in pairs (the maximum of one list with the other reversed holds the best KM of
+// both, as a bitonic sequence).
 //
 // Scores are recomputed in the backward pass rather than kept: reading T x E logits again
 // costs what reading T x E scores would.
@@ -22,64 +26,131 @@
 namespace dg {
 namespace {
 
-constexpr int kRouteThreads = 256;
-constexpr int kRouteWaves = kRouteThreads / 64;
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
 
-// exp(x) for x <= 0 within about an ulp: 2^(x log2 e) with the rounding of the product
-// put back to first order.  Below -104 (where fp32 has nothing left) the result is 0; NaN
-// stays NaN.
-__device__ __forceinline__ float exp_neg(float x) {
-  constexpr float kLog2e = 1.44269504f, kLog2eLow = 1.92596303e-8f, kLn2 = 0.69314718f;
-  const float y = x < -104.0f ? -104.0f : x;
-  const float t = y * kLog2e;
-  const float r = __builtin_fmaf(y, kLog2eLow, __builtin_fmaf(y, kLog2e, -t));
-  const float p = __builtin_amdgcn_exp2f(t);
-  return __builtin_fmaf(p * kLn2, r, p);
+// --------------------------------------------------------------------------- arithmetic
+constexpr float kLog2e = 1.44269504f;
+
+// exp(x) as 2^(x log2 e): two roundings of the exponent, which cost |x| 2^-24 of the result
+// (the weights that matter have small |x|).  0 at -inf, NaN at NaN.
+__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+
+// sigmoid(z) = s and s (1 - s), without cancellation on either side; 0 at -inf, 1 at inf.
+__device__ __forceinline__ float sigmoid(float z, float* slope) {
+  const float e = exp_of(-fabsf(z));
+  const float r = __builtin_amdgcn_rcpf(1.0f + e), er = e * r;
+  *slope = r * er;
+  return z >= 0.0f ? r : er;
+}
+__device__ __forceinline__ float sigmoid(float z) {
+  float slope;
+  return sigmoid(z, &slope);
 }
 
-// sigmoid(z) and 1 - sigmoid(z), each without cancellation; exact 0 and 1 at -inf and inf.
-__device__ __forceinline__ void sigmoid(float z, float* s, float* c) {
-  const float e = exp_neg(-fabsf(z));
-  const float r = 1.0f / (1.0f + e);
-  const float er = e * r;
-  *s = z >= 0.0f ? r : er;
-  *c = z >= 0.0f ? er : r;
-  if (z != z) *s = *c = z;
+// ------------------------------------------------------------------------ across lanes
+// The value of another lane of the group, for combining groups of X lanes (whose lanes all
+// hold the same) into groups of 2 X: lane ^ X, or any other lane of the other half.
+template <int X>
+__device__ __forceinline__ int across(int v) {
+  if constexpr (X == 1) return __builtin_amdgcn_mov_dpp(v, 0xB1, 0xF, 0xF, true);    // quad 1 0 3 2
+  else if constexpr (X == 2) return __builtin_amdgcn_mov_dpp(v, 0x4E, 0xF, 0xF, true);  // 2 3 0 1
+  else if constexpr (X == 4) return __builtin_amdgcn_mov_dpp(v, 0x141, 0xF, 0xF, true); // 8 mirrored
+  else if constexpr (X == 8) return __builtin_amdgcn_mov_dpp(v, 0x140, 0xF, 0xF, true); // 16 mirrored
+  else return __shfl_xor(v, X, 64);
+}
+template <int X>
+__device__ __forceinline__ float across(float v) {
+  return __int_as_float(across<X>(__float_as_int(v)));
+}
+template <int X>
+__device__ __forceinline__ double across(double v) {
+  const long long u = __double_as_longlong(v);
+  const uint32_t lo = (uint32_t)across<X>((int)(uint32_t)u), hi = (uint32_t)across<X>((int)(u >> 32));
+  return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
 }
 
-template <int L>
+template <int L, int X = 1>
 __device__ __forceinline__ float group_max(float v) {
-#pragma unroll
-  for (int off = L / 2; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, L));
-  return v;
+  if constexpr (X < L) return group_max<L, 2 * X>(fmaxf(v, across<X>(v)));
+  else return v;
 }
-template <int L>
+template <int L, int X = 1>
 __device__ __forceinline__ float group_sum(float v) {
-#pragma unroll
-  for (int off = L / 2; off >= 1; off >>= 1) v += __shfl_xor(v, off, L);
-  return v;
-}
-template <int L>
-__device__ __forceinline__ double group_max(double v) {
-#pragma unroll
-  for (int off = L / 2; off >= 1; off >>= 1) v = fmax(v, __shfl_xor(v, off, L));
-  return v;
+  if constexpr (X < L) return group_sum<L, 2 * X>(v + across<X>(v));
+  else return v;
 }
 
-constexpr double kNoKey = -1.0e300;       // below every widened fp32 key
-
-// The key of expert e as described above; -inf and NaN keys cannot be chosen.
+// --------------------------------------------------------------------- choosing experts
 __device__ __forceinline__ double pack_key(float key, int e) {
-  if (!(key > -INFINITY)) return kNoKey;
-  const double d = key == INFINITY ? 1.0e300 : (double)(key + 0.0f);   // -0 counts as 0
-  const uint64_t u = (uint64_t)__double_as_longlong(d) & ~(uint64_t)1023;
-  return __longlong_as_double((long long)(u | (uint64_t)(d < 0.0 ? e : 1023 - e)));
+  const int bits = __float_as_int(fmaxf(key, -INFINITY));      // NaN: -inf
+  const uint32_t low = (uint32_t)((bits >> 31) ^ (1023 - e));
+  return __longlong_as_double((long long)(((uint64_t)(uint32_t)bits << 32) | low));
 }
-__device__ __forceinline__ int key_expert(double d) {
-  const int low = (int)(__double_as_longlong(d) & 1023);
-  return d <= kNoKey ? -1 : (d < 0.0 ? low : 1023 - low);
+__device__ __forceinline__ double no_key() {                   // below every finite key
+  return __longlong_as_double((long long)0xFF800000FFFFFFFFull);
+}
+__device__ __forceinline__ float key_value(double d) {
+  return __int_as_float((int)(__double_as_longlong(d) >> 32));
+}
+__device__ __forceinline__ int key_expert(double d) {          // -1: a key of -inf
+  const int bits = (int)(__double_as_longlong(d) >> 32);
+  const int low = (int)__double_as_longlong(d);
+  return bits == (int)0xFF800000 ? -1 : 1023 - (low ^ (bits >> 31));
 }
 
+__device__ __forceinline__ void order(double& a, double& b) {  // a >= b
+  const double hi = fmax(a, b), lo = fmin(a, b);
+  a = hi;
+  b = lo;
+}
+
+// Comparators of an odd-even merge sort of N = 2^n numbers.
+template <int N>
+struct SortNet {
+  int n = 0;
+  int a[80] = {}, b[80] = {};
+  constexpr SortNet() {
+    for (int p = 1; p < N; p *= 2)
+      for (int k = p; k >= 1; k /= 2)
+        for (int j = k % p; j + k < N; j += 2 * k)
+          for (int i = 0; i < k && i + j + k < N; ++i)
+            if ((i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+              a[n] = i + j;
+              b[n] = i + j + k;
+              ++n;
+            }
+  }
+};
+template <int N>
+__device__ __forceinline__ void sort(double (&x)[N]) {
+  constexpr SortNet<N> net;
+#pragma unroll
+  for (int t = 0; t < net.n; ++t) order(x[net.a[t]], x[net.b[t]]);
+}
+// list = the best N of list and other (given in reverse), both sorted
+template <int N>
+__device__ __forceinline__ void merge(double (&list)[N], const double (&other)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) list[i] = fmax(list[i], other[N - 1 - i]);
+#pragma unroll
+  for (int d = N / 2; d >= 1; d /= 2)
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if ((i & d) == 0) order(list[i], list[i + d]);
+}
+template <int L, int N, int X = 1>
+__device__ __forceinline__ void merge_lanes(double (&list)[N]) {
+  if constexpr (X < L) {
+    double other[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) other[i] = across<X>(list[i]);
+    merge<N>(list, other);
+    merge_lanes<L, N, 2 * X>(list);
+  }
+}
+
+// ------------------------------------------------------------------------------- memory
 __device__ __forceinline__ float load_one(const void* p, int64_t i, int bf16) {
   return bf16 ? __uint_as_float((uint32_t)((const uint16_t*)p)[i] << 16) : ((const float*)p)[i];
 }
@@ -120,7 +191,8 @@ __device__ __forceinline__ void load_row(const RouteArgs& a, int64_t row, int l,
 }
 
 // A row's softmax: its maximum and 1 / sum of exp(z - max), by which a score is
-// exp(z - max) * inv.  A row of -inf only (nothing left of it) has max = 0 and inv = 0.
+// exp(z - max) * inv; s = exp(z - max).  A row of -inf only (nothing left of it) has max = 0
+// and inv = 0.
 struct RowNorm {
   float max, inv;
 };
@@ -136,7 +208,7 @@ __device__ __forceinline__ RowNorm softmax_row(const float (&z)[V], float (&s)[V
   float sum = 0.0f;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    s[v] = exp_neg(z[v] - m);
+    s[v] = exp_of(z[v] - m);
     sum += s[v];
   }
   sum = group_sum<L>(sum);
@@ -144,97 +216,121 @@ __device__ __forceinline__ RowNorm softmax_row(const float (&z)[V], float (&s)[V
 }
 
 // ------------------------------------------------------------------------------ forward
-// Grid-stride over row blocks.  With `counts` every workgroup leaves its sums over its
-// rows (chosen rows and, with `loss`, probabilities of each expert, live rows) in the
-// workspace, and the last workgroup to arrive adds them up in workgroup order: the result
-// does not depend on which one that is.
-template <int L, int V>
-__global__ void __launch_bounds__(kRouteThreads)
+// What the workgroups of a call with several have counted, in the workspace: [workgroup][E]
+// probabilities, [workgroup][E] choices, [workgroup] live rows; before them the second
+// kernel's arrival counter and its workgroups' parts of the loss.
+struct Parts {
+  int* arrivals;
+  float* loss;
+  float* p;
+  int* n;
+  int* rows;
+  __device__ Parts(const RouteArgs& a, int G)
+      : arrivals((int*)a.workspace),
+        loss((float*)a.workspace + 1),
+        p((float*)((uint8_t*)a.workspace + kRouteWsHeader)),
+        n((int*)(p + (int64_t)G * a.E)),
+        rows(n + (int64_t)G * a.E) {}
+};
+
+__device__ __forceinline__ float coef_of(const RouteArgs& a, int n, int live) {
+  const float rows = (float)live;
+  return live ? a.balance * (float)a.E / (float)a.k * (float)n / rows / rows : 0.0f;
+}
+
+// A call of one workgroup ends with the sums over rows; the workgroups of a larger one leave
+// theirs to route_sums_kernel.
+template <int L, int V, int KM>
+__global__ void __launch_bounds__(kThreads, V == 32 ? 3 : 4)
 route_kernel(RouteArgs a) {
   constexpr int RW = 64 / L, EP = L * V;
+  constexpr int KP = KM > L ? KM / L : 1;             // choices that a lane writes
   __shared__ int hist[EP];
-  __shared__ float psum[kRouteWaves][EP];
+  __shared__ __attribute__((aligned(16))) float psum[kWaves * RW][EP];
+  __shared__ __attribute__((aligned(16))) float bias[EP];
   __shared__ int live_rows;
-  __shared__ int is_last;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int l = lane % L, sub = lane / L;
   const bool sums = a.counts != nullptr;
-  for (int e = tid; e < EP; e += kRouteThreads) hist[e] = 0;
+  for (int e = tid; e < EP; e += kThreads) {
+    hist[e] = 0;
+    bias[e] = a.bias && e < a.E ? a.bias[e] : 0.0f;
+  }
   if (tid == 0) live_rows = 0;
   __syncthreads();
 
-  float bias[V], acc[V];
+  float acc[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int e = 4 * ((v / 4) * L + l) + (v & 3);
-    bias[v] = a.bias && e < a.E ? a.bias[e] : 0.0f;
-    acc[v] = 0.0f;
-  }
+  for (int v = 0; v < V; ++v) acc[v] = 0.0f;
   int nlive = 0;
-  const int64_t step = (int64_t)gridDim.x * kRouteWaves * RW;
-  for (int64_t row0 = ((int64_t)blockIdx.x * kRouteWaves + wave) * RW; row0 < a.T; row0 += step) {
+  const int64_t step = (int64_t)gridDim.x * kWaves * RW;
+  for (int64_t row0 = ((int64_t)blockIdx.x * kWaves + wave) * RW; row0 < a.T; row0 += step) {
     const int64_t row = row0 + sub;
     const bool in = row < a.T;
-    const bool live = in && (!a.row_valid || a.row_valid[row] != 0);
+    const int64_t at = in ? row : a.T - 1;
     float z[V], s[V];
-    if (live) {
-      load_row<L, V>(a, row, l, -INFINITY, z);
-    } else {
+    load_row<L, V>(a, at, l, -INFINITY, z);
+    const bool live = in && (!a.row_valid || a.row_valid[at] != 0);
 #pragma unroll
-      for (int v = 0; v < V; ++v) z[v] = -INFINITY;
-    }
-    RowNorm n{0.0f, 0.0f};
-    if (a.sigmoid) {
-      if (a.loss) {
-        float sum = 0.0f;
+    for (int v = 0; v < V; ++v) z[v] = live ? z[v] : -INFINITY;
+    if (live && l == 0) ++nlive;
+
+    // the best KM keys of the row, in every lane of it
+    double list[KM];
+    constexpr int NB = KM < V ? KM : V;               // candidates sorted at a time
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          float c;
-          sigmoid(z[v], &s[v], &c);
-          sum += s[v];
-        }
-        sum = group_sum<L>(sum);
-        n.inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    for (int b = 0; b < V / NB; ++b) {
+      __builtin_amdgcn_sched_barrier(0);              // one block's candidates at a time
+      double x[NB];
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        const int v = b * NB + i, e = 4 * ((v / 4) * L + l) + (v & 3);
+        x[i] = pack_key(z[v] + bias[e], e);
       }
-    } else {
+      sort<NB>(x);
+      if (b == 0) {
+#pragma unroll
+        for (int i = 0; i < KM; ++i) list[i] = i < NB ? x[i < NB ? i : 0] : no_key();
+      } else if constexpr (NB == KM) {
+        merge<KM>(list, x);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    merge_lanes<L, KM>(list);
+    __builtin_amdgcn_sched_barrier(0);
+
+    RowNorm n{0.0f, 0.0f};
+    if (!a.sigmoid) {
       n = softmax_row<L, V>(z, s);
+    } else if (a.loss) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        s[v] = sigmoid(z[v]);
+        sum += s[v];
+      }
+      sum = group_sum<L>(sum);
+      n.inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     }
     if (a.loss) {
 #pragma unroll
       for (int v = 0; v < V; ++v) acc[v] = __builtin_fmaf(s[v], n.inv, acc[v]);
     }
-    double key[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) key[v] = pack_key(z[v] + bias[v], 4 * ((v / 4) * L + l) + (v & 3));
-    if (live && l == 0) ++nlive;
 
-    // k rounds: the largest key left; lane j % L keeps the choices j, j + L, ...
-    constexpr int KP = L >= kRouteMaxK ? 1 : kRouteMaxK / L;
+    // lane l of the row keeps the choices l, l + L, ...
     int ids[KP];
-#pragma unroll
-    for (int q = 0; q < KP; ++q) ids[q] = -1;
-    for (int j = 0; j < a.k; ++j) {
-      double m = key[0];
-#pragma unroll
-      for (int v = 1; v < V; ++v) m = fmax(m, key[v]);
-      m = group_max<L>(m);
-#pragma unroll
-      for (int v = 0; v < V; ++v) key[v] = key[v] == m ? kNoKey : key[v];
-      const int e = key_expert(m);
-#pragma unroll
-      for (int q = 0; q < KP; ++q)
-        if (j == q * L + l) ids[q] = e;
-    }
-    // scores of the chosen experts, recomputed by the lane that keeps each
     float w[KP], total = 0.0f;
 #pragma unroll
     for (int q = 0; q < KP; ++q) {
+      const int j = q * L + l;
+      double d = list[0];
+#pragma unroll
+      for (int i = 1; i < KM; ++i) d = j == i ? list[i] : d;
+      ids[q] = j < a.k ? key_expert(d) : -1;
       w[q] = 0.0f;
       if (ids[q] >= 0) {
-        const float zc = load_one(a.logits, row * a.ld + ids[q], a.bf16);
-        float c;
-        if (a.sigmoid) sigmoid(zc, &w[q], &c);
-        else w[q] = exp_neg(zc - n.max) * n.inv;
+        const float zc = a.bias ? load_one(a.logits, at * a.ld + ids[q], a.bf16) : key_value(d);
+        w[q] = a.sigmoid ? sigmoid(zc) : exp_of(zc - n.max) * n.inv;
         if (sums) atomicAdd(&hist[ids[q]], 1);
       }
       total += w[q];
@@ -255,89 +351,135 @@ route_kernel(RouteArgs a) {
   }
   if (!sums) return;
 
-  // this workgroup's sums
-  atomicAdd(&live_rows, nlive);
+  // the workgroup's sums, the probabilities in the order of its rows' places
+  if (l == 0) atomicAdd(&live_rows, nlive);
   if (a.loss) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      float p = acc[v];
-#pragma unroll
-      for (int off = 32; off >= L; off >>= 1) p += __shfl_xor(p, off, 64);
-      if (sub == 0) psum[wave][4 * ((v / 4) * L + l) + (v & 3)] = p;
-    }
+    for (int c = 0; c < V / 4; ++c)
+      *(float4*)&psum[wave * RW + sub][4 * (c * L + l)] =
+          make_float4(acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]);
   }
   __syncthreads();
   const int G = (int)gridDim.x, b = blockIdx.x;
-  float* part_p = (float*)((uint8_t*)a.workspace + kRouteWsHeader);
-  int* part_n = (int*)(part_p + (int64_t)G * a.E);
-  int* part_live = part_n + (int64_t)G * a.E;
-  for (int e = tid; e < a.E; e += kRouteThreads) {
-    if (a.loss) {
-      float p = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kRouteWaves; ++w) p += psum[w][e];
-      __hip_atomic_store(part_p + (int64_t)b * a.E + e, p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-    __hip_atomic_store(part_n + (int64_t)b * a.E + e, hist[e], __ATOMIC_RELAXED,
-                       __HIP_MEMORY_SCOPE_AGENT);
-  }
-  if (tid == 0)
-    __hip_atomic_store(part_live + b, live_rows, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  __threadfence();                      // this thread's stores before its workgroup's arrival
-  __syncthreads();
-  if (tid == 0)
-    is_last = __hip_atomic_fetch_add((int*)a.workspace, 1, __ATOMIC_ACQ_REL,
-                                     __HIP_MEMORY_SCOPE_AGENT) == G - 1;
-  __syncthreads();
-  if (!is_last) return;
-  __threadfence();
-  if (tid == 0) {
-    __hip_atomic_store((int*)a.workspace, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    live_rows = 0;
-  }
-  __syncthreads();
-  for (int g = tid; g < G; g += kRouteThreads)
-    atomicAdd(&live_rows, __hip_atomic_load(part_live + g, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
-  __syncthreads();
-  const float rows = (float)live_rows;
-  float part = 0.0f;
-  for (int e = tid; e < a.E; e += kRouteThreads) {
-    int n = 0;
+  Parts part(a, G);
+  float sum = 0.0f;
+  for (int e = tid; e < a.E; e += kThreads) {
+    const int n = hist[e];
     float p = 0.0f;
-    for (int g = 0; g < G; ++g) {
-      n += __hip_atomic_load(part_n + (int64_t)g * a.E + e, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      if (a.loss)
-        p += __hip_atomic_load(part_p + (int64_t)g * a.E + e, __ATOMIC_RELAXED,
-                               __HIP_MEMORY_SCOPE_AGENT);
+    if (a.loss)
+      for (int w = 0; w < kWaves * RW; ++w) p += psum[w][e];
+    if (G > 1) {
+      part.n[(int64_t)b * a.E + e] = n;
+      if (a.loss) part.p[(int64_t)b * a.E + e] = p;
+    } else {
+      a.counts[e] = n;
+      if (a.loss) {
+        const float c = coef_of(a, n, live_rows);
+        a.coef[e] = c;
+        sum += live_rows ? c * p : 0.0f;
+      }
+    }
+  }
+  if (G > 1) {
+    if (tid == 0) part.rows[b] = live_rows;
+    if (tid == 0 && b == 0) *part.arrivals = 0;
+  } else if (a.loss) {
+    sum = group_sum<64>(sum);
+    __syncthreads();
+    if (lane == 0) bias[wave] = sum;
+    __syncthreads();
+    if (tid == 0) *a.loss = (bias[0] + bias[1]) + (bias[2] + bias[3]);
+  }
+}
+
+// Sums over the first kernel's G workgroups: a workgroup takes `cols` experts, its threads
+// one of them and a slice of the G each, then the slices in order.  Of the loss's parts the
+// last workgroup to arrive takes the sum, in workgroup order.
+constexpr int kSumThreads = 1024, kSumMinCols = 16;
+
+__global__ void __launch_bounds__(kSumThreads)
+route_sums_kernel(RouteArgs a, int G, int cols) {
+  __shared__ int n_s[kSumThreads], live_s[kSumThreads / 64];
+  __shared__ float p_s[kSumThreads];
+  __shared__ int last;
+  const int tid = threadIdx.x, c = tid & (cols - 1), slices = kSumThreads / cols, slice = tid / cols;
+  const int e = blockIdx.x * cols + c, ee = e < a.E ? e : a.E - 1;
+  Parts part(a, G);
+  int n = 0, live = 0;
+  float p = 0.0f;
+#pragma unroll 8
+  for (int g = slice; g < G; g += slices) n += part.n[(int64_t)g * a.E + ee];
+  if (a.loss) {
+#pragma unroll 8
+    for (int g = slice; g < G; g += slices) p += part.p[(int64_t)g * a.E + ee];
+  }
+  if (tid < G) live = part.rows[tid];
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) live += __shfl_xor(live, off, 64);
+  n_s[tid] = n;
+  p_s[tid] = p;
+  if ((tid & 63) == 0) live_s[tid >> 6] = live;
+  __syncthreads();
+  live = 0;
+  for (int w = 0; w < kSumThreads / 64; ++w) live += live_s[w];
+  float sum = 0.0f;
+  if (tid < cols && e < a.E) {
+    for (int w = 1; w < slices; ++w) {
+      n += n_s[w * cols + tid];
+      p += p_s[w * cols + tid];
     }
     a.counts[e] = n;
     if (a.loss) {
-      const float c = live_rows ? a.balance * (float)a.E / (float)a.k * (float)n / rows / rows : 0.0f;
-      a.coef[e] = c;
-      part += live_rows ? c * p : 0.0f;
+      const float cf = coef_of(a, n, live);
+      a.coef[e] = cf;
+      sum = live ? cf * p : 0.0f;
     }
   }
-  if (a.loss) {
-    part = group_sum<64>(part);
-    if (lane == 0) psum[wave][0] = part;
-    __syncthreads();
+  if (!a.loss) return;
+  sum = group_sum<64>(sum);
+  __syncthreads();
+  if ((tid & 63) == 0) p_s[tid >> 6] = sum;
+  __syncthreads();
+  if (tid >= 64) return;
+  sum = group_sum<16>(p_s[tid & 15]);
+  const int B = (int)gridDim.x;
+  if (B > 1) {
+    // handed over with device-coherent accesses: stores complete before the arrival
     if (tid == 0) {
-      float sum = 0.0f;
-      for (int w = 0; w < kRouteWaves; ++w) sum += psum[w][0];
-      *a.loss = sum;
+      __hip_atomic_store(part.loss + blockIdx.x, sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      last = __hip_atomic_fetch_add(part.arrivals, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+             B - 1;
     }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    if (!last) return;
+    sum = tid < B ? __hip_atomic_load(part.loss + tid, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0.0f;
+    sum = group_sum<64>(sum);
   }
+  if (tid == 0) *a.loss = sum;
 }
+
+// Experts of a workgroup of the second kernel: at most about 16 of the G sums a thread.
+int sum_cols(int E, int G) {
+  int cols = kSumMinCols;
+  while (cols < E && cols < kSumThreads && 2 * cols * G <= 16 * kSumThreads) cols *= 2;
+  return cols;
+}
+static_assert(kRouteMaxGrid <= kSumThreads, "one thread a workgroup's live rows");
+static_assert((kRouteMaxE + kSumMinCols - 1) / kSumMinCols <= 64, "one lane a part of the loss");
+static_assert(4 * (1 + 64) <= kRouteWsHeader, "header");
 
 // ----------------------------------------------------------------------------- backward
 // dz from the weights' gradients (scattered to the chosen experts through a row of LDS)
 // and the loss's (coef, the same for every row).
 template <int L, int V>
-__global__ void __launch_bounds__(kRouteThreads)
+__global__ void __launch_bounds__(kThreads)
 route_backward_kernel(RouteArgs a) {
   constexpr int RW = 64 / L, EP = L * V;
   constexpr int KP = L >= kRouteMaxK ? 1 : kRouteMaxK / L;
-  __shared__ float rows_d[kRouteWaves * RW][EP];
+  __shared__ float rows_d[kWaves * RW][EP];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int l = lane % L, sub = lane / L;
   float* d = rows_d[wave * RW + sub];
@@ -351,8 +493,8 @@ route_backward_kernel(RouteArgs a) {
     const int e = 4 * ((v / 4) * L + l) + (v & 3);
     u[v] = a.coef && e < a.E ? g_loss * a.coef[e] : 0.0f;
   }
-  const int64_t step = (int64_t)gridDim.x * kRouteWaves * RW;
-  for (int64_t row0 = ((int64_t)blockIdx.x * kRouteWaves + wave) * RW; row0 < a.T; row0 += step) {
+  const int64_t step = (int64_t)gridDim.x * kWaves * RW;
+  for (int64_t row0 = ((int64_t)blockIdx.x * kWaves + wave) * RW; row0 < a.T; row0 += step) {
     const int64_t row = row0 + sub;
     const bool in = row < a.T;
     const bool live = in && (!a.row_valid || a.row_valid[row] != 0);
@@ -369,7 +511,7 @@ route_backward_kernel(RouteArgs a) {
       float sum = 0.0f;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        sigmoid(z[v], &s[v], &c[v]);
+        s[v] = sigmoid(z[v], &c[v]);
         sum += s[v];
         us = __builtin_fmaf(u[v], s[v], us);
       }
@@ -399,9 +541,7 @@ route_backward_kernel(RouteArgs a) {
           id[q] = e;
           gw[q] = a.scale * a.grad_weights[row * a.k + j];
           const float zc = load_one(a.logits, row * a.ld + e, a.bf16);
-          float cc;
-          if (a.sigmoid) sigmoid(zc, &sc[q], &cc);
-          else sc[q] = exp_neg(zc - n.max) * n.inv;
+          sc[q] = a.sigmoid ? sigmoid(zc) : exp_of(zc - n.max) * n.inv;
         }
       }
       total += sc[q];
@@ -430,7 +570,7 @@ route_backward_kernel(RouteArgs a) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const float dv = d[4 * ((v / 4) * L + l) + (v & 3)];
-      dz[v] = a.sigmoid ? ((u[v] - us) * n.inv + dv) * s[v] * c[v] : s[v] * (u[v] + dv - (us + ds));
+      dz[v] = a.sigmoid ? ((u[v] - us) * n.inv + dv) * c[v] : s[v] * (u[v] + dv - (us + ds));
     }
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
@@ -468,33 +608,87 @@ route_backward_kernel(RouteArgs a) {
 }
 
 template <int L, int V>
-void launch(const RouteArgs& a, bool backward, int grid, hipStream_t stream) {
-  if (backward)
-    hipLaunchKernelGGL((route_backward_kernel<L, V>), dim3(grid), dim3(kRouteThreads), 0, stream, a);
-  else
-    hipLaunchKernelGGL((route_kernel<L, V>), dim3(grid), dim3(kRouteThreads), 0, stream, a);
+void launch_forward(const RouteArgs& a, int grid, hipStream_t stream) {
+  const int k = a.k;
+  auto* f = k <= 2   ? &route_kernel<L, V, 2>
+            : k <= 4 ? &route_kernel<L, V, 4>
+            : k <= 8 ? &route_kernel<L, V, 8>
+                     : &route_kernel<L, V, 16>;
+  hipLaunchKernelGGL(f, dim3(grid), dim3(kThreads), 0, stream, a);
+  if (a.counts && grid > 1) {
+    const int cols = sum_cols(a.E, grid);
+    hipLaunchKernelGGL(route_sums_kernel, dim3((a.E + cols - 1) / cols), dim3(kSumThreads), 0, stream,
+                       a, grid, cols);
+  }
 }
 
-// Lanes a row: as few as hold it at 16 experts each.
-int lanes_of(int64_t E) {
-  return E <= 64 ? 4 : E <= 128 ? 8 : E <= 256 ? 16 : E <= 512 ? 32 : 64;
+template <int L, int V>
+void launch_backward(const RouteArgs& a, int grid, hipStream_t stream) {
+  hipLaunchKernelGGL((route_backward_kernel<L, V>), dim3(grid), dim3(kThreads), 0, stream, a);
+}
+
+int lanes_for(int64_t E, int V) {
+  int L = 1;
+  while (L * V < E) L *= 2;
+  return L;
+}
+
+// Forward launch shape.  Few experts a lane (V = 8) spread a row over more lanes: shorter
+// chains, for calls that do not fill the GPU.  Many (V = 32) leave less to merge across
+// lanes: less work in all.
+struct Shape {
+  int V, L, grid;
+};
+Shape forward_shape(int64_t T, int64_t E) {
+  Shape h;
+  h.V = E > 512 || T * E >= kRouteWideWork ? 32 : 8;
+  h.L = lanes_for(E, h.V);
+  if (h.V == 32 && h.L < 2) h.L = 2;
+  const int64_t rows = (int64_t)kWaves * 64 / h.L, blocks = (T + rows - 1) / rows;
+  h.grid = (int)(blocks < 1 ? 1 : blocks < kRouteMaxGrid ? blocks : kRouteMaxGrid);
+  return h;
 }
 
 }  // namespace
 
-int route_grid(int64_t T, int64_t E) {
-  const int64_t rows = (int64_t)kRouteWaves * 64 / lanes_of(E);
-  const int64_t blocks = (T + rows - 1) / rows;
-  return (int)(blocks < 1 ? 1 : blocks < kRouteMaxGrid ? blocks : kRouteMaxGrid);
+int route_slots(int64_t T, int64_t E) {
+  const int g = forward_shape(T, E).grid;
+  return g > 1 ? g : 0;
 }
 
-void launch_route(const RouteArgs& a, bool backward, int grid, hipStream_t stream) {
-  switch (lanes_of(a.E)) {
-    case 4: launch<4, 16>(a, backward, grid, stream); break;
-    case 8: launch<8, 16>(a, backward, grid, stream); break;
-    case 16: launch<16, 16>(a, backward, grid, stream); break;
-    case 32: launch<32, 16>(a, backward, grid, stream); break;
-    default: launch<64, 16>(a, backward, grid, stream); break;
+void launch_route(const RouteArgs& a, hipStream_t stream) {
+  const Shape h = forward_shape(a.T, a.E);
+  if (h.V == 32) {
+    switch (h.L) {
+      case 2: return launch_forward<2, 32>(a, h.grid, stream);
+      case 4: return launch_forward<4, 32>(a, h.grid, stream);
+      case 8: return launch_forward<8, 32>(a, h.grid, stream);
+      case 16: return launch_forward<16, 32>(a, h.grid, stream);
+      default: return launch_forward<32, 32>(a, h.grid, stream);
+    }
+  }
+  switch (h.L) {
+    case 1: return launch_forward<1, 8>(a, h.grid, stream);
+    case 2: return launch_forward<2, 8>(a, h.grid, stream);
+    case 4: return launch_forward<4, 8>(a, h.grid, stream);
+    case 8: return launch_forward<8, 8>(a, h.grid, stream);
+    case 16: return launch_forward<16, 8>(a, h.grid, stream);
+    case 32: return launch_forward<32, 8>(a, h.grid, stream);
+    default: return launch_forward<64, 8>(a, h.grid, stream);
+  }
+}
+
+void launch_route_backward(const RouteArgs& a, hipStream_t stream) {
+  int L = lanes_for(a.E, 16);
+  if (L < 4) L = 4;
+  const int64_t rows = (int64_t)kWaves * 64 / L, blocks = (a.T + rows - 1) / rows;
+  const int grid = (int)(blocks < 512 ? blocks : 512);
+  switch (L) {
+    case 4: return launch_backward<4, 16>(a, grid, stream);
+    case 8: return launch_backward<8, 16>(a, grid, stream);
+    case 16: return launch_backward<16, 16>(a, grid, stream);
+    case 32: return launch_backward<32, 16>(a, grid, stream);
+    default: return launch_backward<64, 16>(a, grid, stream);
   }
 }
 

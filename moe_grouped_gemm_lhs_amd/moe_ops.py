@@ -67,10 +67,8 @@ def _device(t, name):
 
 
 def _workspace(need, device, workspace, stream, raw):
-    """The caller's workspace, or one kept per (device, launch stream) and grown as
-    needed: zero filled when it is allocated, on the launch stream; every call leaves its
-    first 256 bytes zero.  Under graph capture each call gets a fresh one from the graph's
-    memory, zero filled by a kernel inside the graph."""
+    """The caller's workspace, or one kept per (device, launch stream) and grown as needed,
+    whatever it holds.  Under graph capture each call gets one from the graph's memory."""
     if workspace is not None:
         if workspace.device != device or not workspace.is_contiguous():
             raise ValueError(f"workspace must be contiguous and on {device}")
@@ -81,7 +79,7 @@ def _workspace(need, device, workspace, stream, raw):
         return ws, ws.numel()
     st = stream if stream is not None else torch.cuda.current_stream(device)
     with torch.cuda.stream(st):
-        ws = torch.zeros(max(need, 1 << 16), dtype=torch.uint8, device=device)
+        ws = torch.empty(max(need, 1 << 16), dtype=torch.uint8, device=device)
         if not torch.cuda.is_current_stream_capturing():
             # a smaller one was used on this stream only, so the allocator may hand its
             # memory out again in this stream's order

