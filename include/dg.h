@@ -309,7 +309,7 @@ dg_status dg_moe_route_backward(const void *logits, int dtype, int64_t ld,
  * only, whatever other adapters hold.  Sums are fp32; the inner product is kept to 16
  * significant bits or more and the result rounded once, to nearest even.
  *
- * T, N >= 0 (0: nothing to do), K > 0 and K % 128 == 0, K <= 2^22, 8 <= R <= 128 and
+ * T, N >= 0 (0: nothing to do), K > 0 and K % 128 == 0, N, K <= 2^22, 8 <= R <= 128 and
  * R % 8 == 0, L >= 1, ldx % 8 == 0, strides at least the row's length (DG_ERR_SHAPE).
  * X, A, B 16-byte aligned, base and out 2-byte (faster: 16-byte with strides that 8
  * divides).  Workspace: dg_lora_workspace_bytes bytes, 16-byte aligned; it may hold

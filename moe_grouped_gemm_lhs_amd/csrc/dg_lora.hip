@@ -24,39 +24,43 @@ namespace {
 using bf16x8 = __attribute__((ext_vector_type(8))) __bf16;
 using f32x4 = __attribute__((ext_vector_type(4))) float;
 
-constexpr int kTile = 16;                 // rows of a tile
+constexpr int kTile = 16;                 // rows of an MFMA tile
 constexpr int kDownWaves = 8;
-constexpr int kFrags = kLoraDownFrags;    // 32-deep pieces of K that a wave holds
 constexpr int kUpWaves = 4;
-constexpr int kUpCols = 64;               // output columns of a wave
 
 __device__ __forceinline__ f32x4 mfma(const uint4& a, const uint4& b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
                                                  __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-__device__ __forceinline__ uint32_t round_bf16(float f) {
-  const uint32_t u = __float_as_uint(f);
-  if ((u & 0x7FFFFFFFu) > 0x7F800000u) return 0x7FC0u;
-  return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
-}
 __device__ __forceinline__ float from_bf16(uint32_t b) { return __uint_as_float(b << 16); }
 
-// The adapters of a tile: lane l holds the id of row l % 16 (-1: none).  next() gives the
-// adapters one by one, in the order of their first rows, with the rows that are theirs.
+// Two fp32 numbers rounded to bf16 (to nearest even), the first in the low half.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  using bf16x2 = __attribute__((ext_vector_type(2))) __bf16;
+  return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)lo, (__bf16)hi});
+}
+
+// The adapters that M <= 64 rows from t0 name, those with id = q modulo Q (a power of two)
+// only: lane l holds the id of row l % M (-1: none).  next() gives them one by one, in the
+// order of their first rows, with the rows that are theirs.
+template <int M>
 struct TileAdapters {
-  int id;                  // of row lane % 16
-  uint32_t left;           // rows whose adapter has not been given out
-  __device__ __forceinline__ TileAdapters(const LoraArgs& a, int64_t t0, int lane) {
-    const int64_t t = t0 + (lane & 15);
-    int i = t < a.T ? a.ids[t] : -1;
+  static constexpr uint64_t kRows = M == 64 ? ~0ull : (1ull << (M & 63)) - 1;
+  int id;
+  uint64_t own, none;      // rows of these adapters; rows without an adapter
+  uint64_t left;           // rows whose adapter has not been given out
+  __device__ __forceinline__ TileAdapters(const LoraArgs& a, int64_t t0, int lane, int q, int Q) {
+    const int64_t t = t0 + (lane & (M - 1));
+    const int i = t < a.T ? a.ids[t] : -1;
     id = i >= 0 && i < a.L ? i : -1;
-    left = (uint32_t)__builtin_amdgcn_ballot_w64(id >= 0) & 0xFFFFu;
+    own = left = __builtin_amdgcn_ballot_w64(id >= 0 && (id & (Q - 1)) == q) & kRows;
+    none = __builtin_amdgcn_ballot_w64(id < 0 && t < a.T) & kRows;
   }
-  __device__ __forceinline__ bool next(int* adapter, uint32_t* rows) {
+  __device__ __forceinline__ bool next(int* adapter, uint64_t* rows) {
     if (!left) return false;
-    *adapter = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
-    *rows = (uint32_t)__builtin_amdgcn_ballot_w64(id == *adapter) & 0xFFFFu;
+    *adapter = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
+    *rows = __builtin_amdgcn_ballot_w64(id == *adapter) & kRows;
     left &= ~*rows;
     return true;
   }
@@ -68,198 +72,586 @@ __device__ __forceinline__ int rank_of(const LoraArgs& a, int adapter) {
   return r < 0 ? 0 : r < a.R ? r : a.R;
 }
 
-// h of a tile's rows over one share of K: workgroup (tile, share s, q) takes every
-// down_q-th adapter of the tile, its waves an eighth each of the share, and the waves'
-// sums are added up in wave order.  A row of h without an adapter is not written.
-__global__ void __launch_bounds__(64 * kDownWaves)
-lora_down_kernel(LoraArgs a) {
-  extern __shared__ float red[];          // [wave][rank tile][row][rank]
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int l16 = lane & 15, g = lane >> 4;
-  const int tile = blockIdx.x, s = blockIdx.y, q = blockIdx.z;
-  const int64_t t0 = (int64_t)tile * kTile;
-  const int rt_all = (a.R + 15) / 16;
-  TileAdapters ad(a, t0, lane);
-
-  // this wave's pieces of K
-  const int pieces = a.K / 32, shares = a.S * kDownWaves, share = s * kDownWaves + wave;
-  const int f0 = (int)((int64_t)pieces * share / shares);
-  const int nf = (int)((int64_t)pieces * (share + 1) / shares) - f0;
-  const int64_t row = t0 + l16 < a.T ? t0 + l16 : a.T - 1;
-  uint4 xf[kFrags];
-  const uint16_t* xp = a.x + row * a.ldx + (int64_t)f0 * 32 + g * 8;
-  bool loaded = false;
-
-  int adapter;
-  uint32_t rows;
-  for (int n = 0; ad.next(&adapter, &rows); ++n) {
-    if (n % a.Q != q) continue;
-    if (!loaded) {
-      loaded = true;
+// nf pieces (64 deep, two instructions) of the products of NA row tiles with RT rank tiles.
+// xp: this lane's row of each row tile; ap: its row of each rank tile.  A lane takes 32
+// consecutive bytes of a piece, half for each instruction (x and A alike, so that the
+// products pair up), and the four lane groups a 128-byte line.  U pieces are in flight
+// while the ones before them are multiplied.
+template <int NA, int RT>
+__device__ __forceinline__ void down_products(const uint16_t* const (&xp)[NA],
+                                              const uint16_t* const (&ap)[RT], int nf,
+                                              f32x4 (&acc)[NA][RT]) {
+  constexpr int U = NA + RT <= 2 ? 4 : NA + RT <= 4 ? 2 : 1;
+  uint4 x[2][U][NA][2], w[2][U][RT][2];
+  // pieces past the last repeat it and are not multiplied
+  auto load = [&](int b, int f) {
 #pragma unroll
-      for (int f = 0; f < kFrags; ++f)
-        if (f < nf) xf[f] = *(const uint4*)(xp + f * 32);
-    }
-    const int r = rank_of(a, adapter), rts = (r + 15) / 16;
-    const float scale = a.scales ? a.scales[adapter] : 1.0f;
-    for (int rt = 0; rt < rts; ++rt) {
-      const int rr = rt * 16 + l16 < a.R ? rt * 16 + l16 : a.R - 1;
-      const uint16_t* ap = a.A + ((int64_t)adapter * a.R + rr) * a.K + (int64_t)f0 * 32 + g * 8;
-      f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int u = 0; u < U; ++u) {
+      const int at = (f + u < nf ? f + u : nf - 1) * 64;
 #pragma unroll
-      for (int f = 0; f < kFrags; ++f)
-        if (f < nf) acc = mfma(xf[f], *(const uint4*)(ap + f * 32), acc);
-      // row 4g + j, rank l16
+      for (int m = 0; m < NA; ++m)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        red[((wave * rt_all + rt) * kTile + 4 * g + j) * 16 + l16] = acc[j];
+        for (int i = 0; i < 2; ++i) x[b][u][m][i] = *(const uint4*)(xp[m] + at + 8 * i);
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) w[b][u][r][i] = *(const uint4*)(ap[r] + at + 8 * i);
     }
-    __syncthreads();
-    for (int i = tid; i < rt_all * 256; i += 64 * kDownWaves) {
-      const int rt = i >> 8, m = (i >> 4) & 15, c = rt * 16 + (i & 15);
-      if (c >= a.R || !((rows >> m) & 1)) continue;
-      float sum = 0.0f;
-      if (c < r)
-        for (int w = 0; w < kDownWaves; ++w)
-          sum += red[((w * rt_all + rt) * kTile + m) * 16 + (i & 15)];
-      a.h[((int64_t)s * a.T + t0 + m) * a.R + c] = sum * scale;
+  };
+  auto multiply = [&](int b, int f) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (f + u >= nf) break;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int m = 0; m < NA; ++m)
+#pragma unroll
+          for (int r = 0; r < RT; ++r) acc[m][r] = mfma(x[b][u][m][i], w[b][u][r][i], acc[m][r]);
     }
-    __syncthreads();
+  };
+  if (nf > 0) load(0, 0);
+  for (int f = 0; f < nf; f += 2 * U) {
+    if (f + U < nf) load(1, f + U);
+    multiply(0, f);
+    if (f + 2 * U < nf) load(0, f + 2 * U);
+    multiply(1, f + U);
   }
 }
 
-// out = base + h B^T for a tile's rows and kUpWaves * kUpCols columns.  Weights are the
-// MFMA's row operand and rows of the tile its columns, so a lane's four results are
-// consecutive output columns; two products over interleaved weights give it eight, one
-// 16-byte load of base and one store.
-template <bool VEC>
-__global__ void __launch_bounds__(64 * kUpWaves)
-lora_up_kernel(LoraArgs a) {
-  extern __shared__ uint16_t hs[];        // [row][2 R rounded up to 32]: rounded, then rest
+// The same for NA of the workgroup's MT row tiles, those with a bit in `tiles`; their sums
+// are left in the leading acc.  Rows of other adapters are not read: their lanes repeat the
+// item's first row.
+template <int NA, int MT, int RT>
+__device__ __forceinline__ void down_tiles(const LoraArgs& a, int64_t t0, uint64_t rows, uint32_t tiles,
+                                           const uint16_t* const (&ap)[RT], int64_t k0, int l16, int nf,
+                                           f32x4 (&acc)[MT][RT]) {
+  const uint16_t* xp[NA];
+  f32x4 sum[NA][RT];
+  const int lead = __builtin_ctzll(rows);
+#pragma unroll
+  for (int m = 0; m < NA; ++m) {
+    const int at = __builtin_ctz(tiles) * kTile + l16;
+    tiles &= tiles - 1;
+    xp[m] = a.x + (t0 + ((rows >> at) & 1 ? at : lead)) * a.ldx + k0;
+#pragma unroll
+    for (int r = 0; r < RT; ++r) sum[m][r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  down_products<NA, RT>(xp, ap, nf, sum);
+#pragma unroll
+  for (int m = 0; m < NA; ++m)
+#pragma unroll
+    for (int r = 0; r < RT; ++r) acc[m][r] = sum[m][r];
+}
+
+// LDS cells for the sums of a workgroup's waves: all eight where that is little, else four,
+// to which the other four add theirs.
+template <int C>
+constexpr int down_slots() { return C <= 4 ? 8 : 4; }
+
+// Part s of h of those of the 16 MT rows from t0 that have a bit in `rows`, all of one
+// adapter: the sum over the pieces [p0, p1) of K.  The workgroup's waves take an eighth of
+// them each; their sums are added up in a fixed order.
+template <int MT, int RT>
+__device__ __forceinline__ void down_item(const LoraArgs& a, int64_t t0, uint64_t rows, int adapter, int s,
+                                          int p0, int p1, float (*red)[MT * RT][kTile * 16]) {
+  constexpr int W = down_slots<MT * RT>();
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, g = lane >> 4;
-  const int64_t t0 = (int64_t)blockIdx.x * kTile;
-  const int64_t n0 = ((int64_t)blockIdx.y * kUpWaves + wave) * kUpCols;
-  TileAdapters ad(a, t0, lane);
-  const int chunks = a.R / 8;             // 8-rank pieces of an adapter
-  const int steps = (2 * chunks + 3) / 4; // MFMA steps over [rounded | rest]
-  const int hw = steps * 32 + 8;          // LDS row, 16 bytes past a multiple of 64
-  const uint32_t mine = ad.left;
-  for (int i = tid; i < kTile * a.R; i += 64 * kUpWaves) {
-    const int m = i / a.R, c = i - m * a.R;
-    float sum = 0.0f;
-    if ((mine >> m) & 1)
-      for (int s = 0; s < a.S; ++s) sum += a.h[((int64_t)s * a.T + t0 + m) * a.R + c];
-    const uint32_t hi = round_bf16(sum);
-    const float rest = sum - from_bf16(hi);
-    hs[m * hw + c] = (uint16_t)hi;
-    hs[m * hw + a.R + c] = (uint16_t)(fabsf(rest) < INFINITY ? round_bf16(rest) : 0u);
+  const int f0 = p0 + (p1 - p0) * wave / kDownWaves;
+  const int nf = p0 + (p1 - p0) * (wave + 1) / kDownWaves - f0;
+  const int64_t k0 = (int64_t)f0 * 64 + g * 16;
+  const int rank = rank_of(a, adapter);
+  const float scale = a.scales ? a.scales[adapter] : 1.0f;
+  uint32_t tiles = 0;
+#pragma unroll
+  for (int m = 0; m < MT; ++m) tiles |= ((rows >> (m * kTile)) & 0xFFFF) ? 1u << m : 0u;
+  f32x4 acc[MT][RT];
+  // ranks past R repeat the last; what A holds past the adapter's rank is multiplied too (to
+  // wait for the rank first costs more) and those sums are not used
+  const uint16_t* ap[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    const int c = r * 16 + l16;
+    ap[r] = a.A + ((int64_t)adapter * a.R + (c < a.R ? c : a.R - 1)) * a.K + k0;
   }
-  for (int i = tid; i < kTile * (steps * 32 - 2 * a.R); i += 64 * kUpWaves) {
-    const int w = steps * 32 - 2 * a.R;
-    hs[(i / w) * hw + 2 * a.R + i % w] = 0;
+  const int na = __builtin_popcount(tiles);
+  if (MT >= 4 && na > 3) down_tiles<MT >= 4 ? 4 : 1, MT, RT>(a, t0, rows, tiles, ap, k0, l16, nf, acc);
+  else if (MT >= 4 && na > 2) down_tiles<MT >= 4 ? 3 : 1, MT, RT>(a, t0, rows, tiles, ap, k0, l16, nf, acc);
+  else if (MT >= 2 && na > 1) down_tiles<MT >= 2 ? 2 : 1, MT, RT>(a, t0, rows, tiles, ap, k0, l16, nf, acc);
+  else down_tiles<1, MT, RT>(a, t0, rows, tiles, ap, k0, l16, nf, acc);
+  // acc[m][r][j]: row 4 g + j of the m-th of `tiles`, rank 16 r + l16; a cell holds its 16
+  // rows rank by rank
+  auto put = [&](int slot, bool add) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      if (m >= na) break;
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        f32x4* p = (f32x4*)&red[slot][m * RT + r][l16 * 16 + 4 * g];
+        *p = add ? *p + acc[m][r] : acc[m][r];
+      }
+    }
+  };
+  if (W == 8) {
+    put(wave, false);
+  } else {
+    if (wave >= 4) put(wave - 4, false);
+    __syncthreads();
+    if (wave < 4) put(wave, true);
+  }
+  __syncthreads();
+  for (int i = tid; i < na * (RT * 64); i += 64 * kDownWaves) {
+    // i: (row tile in `tiles`, four rows, rank), ranks fastest
+    const int c = i % (RT * 16), four = i / (RT * 16), m = four / 4;
+    uint32_t t = tiles;
+    for (int x = 0; x < m; ++x) t &= t - 1;
+    const int at = __builtin_ctz(t) * kTile + (four & 3) * 4;
+    if (c >= a.R || !((rows >> at) & 15)) continue;
+    f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (c < rank) {
+#pragma unroll
+      for (int w = 0; w < W; ++w)
+        sum += *(const f32x4*)&red[w][m * RT + c / 16][(c & 15) * 16 + (four & 3) * 4];
+    }
+    float* h = a.h + s * a.h_part + (t0 + at) * a.R + c;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if ((rows >> (at + j)) & 1) h[(int64_t)j * a.R] = sum[j] * scale;
+  }
+  __syncthreads();
+}
+
+// Few rows: workgroup (row, share).  The row's workgroup works for all rows of the row's
+// adapter in its tile if it is the first of them, and has nothing to do otherwise.
+template <int RT>
+__global__ void __launch_bounds__(64 * kDownWaves, 2)
+lora_down_rows_kernel(LoraArgs a) {
+  __shared__ __attribute__((aligned(16))) float red[down_slots<RT>()][RT][kTile * 16];
+  const int lane = threadIdx.x & 63, at = blockIdx.x & (kTile - 1);
+  const int64_t t0 = blockIdx.x - at, t = t0 + (lane & (kTile - 1));
+  const int id = t < a.T ? a.ids[t] : -1;
+  const int adapter = __builtin_amdgcn_readlane(id, at);
+  const uint64_t rows = __builtin_amdgcn_ballot_w64(id == adapter) & 0xFFFF;
+  if (adapter < 0 || adapter >= a.L || __builtin_ctzll(rows) != at) return;
+  const int pieces = a.K / 64, s = blockIdx.y;
+  down_item<1, RT>(a, t0, rows, adapter, s, (int)((int64_t)pieces * s / a.S),
+                   (int)((int64_t)pieces * (s + 1) / a.S), red);
+}
+
+// Many rows: an item is a run of rows of one adapter within a tile of 16 MT.  Every workgroup
+// counts the items for itself from the ids (64 rows a ballot), without a launch to plan it,
+// and then knows its share of them:
+//  - where dividing each item's K alike gives most workgroups one part, it takes that part;
+//  - otherwise the items' pieces of K, one item after the other, are dealt out evenly.  A
+//    piece is counted as its loads, RT for the adapter's ranks and one for each tile of 16
+//    that the run touches, so the single rows of a mixed batch and the ends of prompts
+//    within a tile cost what they cost.
+// An item's parts, at most a.S, are the workgroups that share it; their number goes to
+// `parts` for each of its rows.
+constexpr int kCounts = 256;              // blocks of rows, at most
+
+__device__ __forceinline__ int row_id(const LoraArgs& a, int64_t t) { return t < a.T ? a.ids[t] : -1; }
+
+// Rows at which a run within a tile of M rows begins, of 64 with these ids.
+template <int M>
+__device__ __forceinline__ uint64_t run_starts(const LoraArgs& a, int lane, int id) {
+  const int before = __shfl_up(id, 1, 64);
+  return __builtin_amdgcn_ballot_w64(id >= 0 && id < a.L && ((lane & (M - 1)) == 0 || before != id));
+}
+
+// The run that begins at row `at`: up to the end of its tile or the first row of another id.
+template <int M>
+__device__ __forceinline__ uint64_t run_rows(int id, int adapter, int at) {
+  const int end = (at & ~(M - 1)) + M;
+  const uint64_t from = ~0ull << at;
+  const uint64_t stop = (__builtin_amdgcn_ballot_w64(id != adapter) | (end < 64 ? ~0ull << end : 0)) & from;
+  return stop ? ((1ull << __builtin_ctzll(stop)) - 1) & from : from;
+}
+
+__device__ __forceinline__ int tiles_of(uint64_t rows) {
+  int n = 0;
+#pragma unroll
+  for (int m = 0; m < 4; ++m) n += (rows >> (16 * m)) & 0xFFFF ? 1 : 0;
+  return n;
+}
+
+template <int MT, int RT>
+__global__ void __launch_bounds__(64 * kDownWaves, 2)
+lora_down_kernel(LoraArgs a) {
+  constexpr int M = MT * kTile, U = 8;
+  __shared__ __attribute__((aligned(16))) float red[down_slots<MT * RT>()][MT * RT][kTile * 16];
+  __shared__ uint32_t items[kCounts + 1], loads[kCounts + 1];   // before a block of `per` times 64 rows
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const uint32_t chunks = (uint32_t)((a.T + 63) / 64);
+  const uint32_t per = (chunks + kCounts - 1) / kCounts;
+  const uint32_t blocks = (chunks + per - 1) / per;
+  for (uint32_t b0 = wave; b0 < blocks; b0 += kDownWaves * U) {
+    uint32_t n[U] = {}, w[U] = {};
+    for (uint32_t c = 0; c < per; ++c) {
+      int id[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        id[u] = row_id(a, (int64_t)((b0 + u * kDownWaves) * per + c) * 64 + lane);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const uint32_t runs = __builtin_popcountll(run_starts<M>(a, lane, id[u]));
+        n[u] += runs;
+        w[u] += RT * runs + __builtin_popcountll(run_starts<kTile>(a, lane, id[u]));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (lane == 0 && b0 + u * kDownWaves < blocks) {
+        items[b0 + u * kDownWaves] = n[u];
+        loads[b0 + u * kDownWaves] = w[u];
+      }
+  }
+  __syncthreads();
+  if (wave < 2) {                         // sums before each block, of one array a wave
+    uint32_t* v = wave ? loads : items;
+    uint32_t before = 0;
+    for (uint32_t b0 = 0; b0 < blocks; b0 += 64) {
+      const uint32_t n = b0 + lane < blocks ? v[b0 + lane] : 0;
+      uint32_t sum = n;
+#pragma unroll
+      for (int off = 1; off < 64; off *= 2) {
+        const uint32_t up = __shfl_up(sum, off, 64);
+        if (lane >= off) sum += up;
+      }
+      if (b0 + lane < blocks) v[b0 + lane] = before + sum - n;
+      before += __shfl(sum, 63, 64);
+    }
+    if (lane == 0) v[blocks] = before;
   }
   __syncthreads();
 
-  const int64_t t = t0 + l16;
-  f32x4 out[4];
-#pragma unroll
-  for (int c = 0; c < 4; ++c) out[c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  int adapter;
-  uint32_t rows;
-  while (ad.next(&adapter, &rows)) {
-    const int r = rank_of(a, adapter);
-    f32x4 acc[4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) acc[c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int st = 0; st < steps; ++st) {
-      const int piece = 4 * st + g;
-      const uint4 hf = *(const uint4*)(hs + l16 * hw + piece * 8);
-      const int rank0 = (piece < chunks ? piece : piece < 2 * chunks ? piece - chunks : chunks) * 8;
-      const int have = r - rank0;         // ranks of this piece that the adapter has
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        // weight row of MFMA row m of product c: its four results per lane group lie at
-        // column 32 (c / 2) + 8 g + 4 (c % 2) + j
-        const int64_t n = n0 + 32 * (c / 2) + 8 * (l16 / 4) + 4 * (c & 1) + (l16 & 3);
-        const int64_t nn = n < a.N ? n : a.N - 1;
-        uint4 b = make_uint4(0, 0, 0, 0);
-        if (have > 0) b = *(const uint4*)(a.B + ((int64_t)adapter * a.N + nn) * a.R + rank0);
-        if (have > 0 && have < 8) {
-          uint32_t w[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            w[i] = 2 * i >= have ? 0u : 2 * i + 1 >= have ? w[i] & 0xFFFFu : w[i];
-          b = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        acc[c] = mfma(b, hf, acc[c]);
-      }
-    }
-    if ((rows >> l16) & 1) {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) out[c] = acc[c];
+  // an item is `span` units of c each, a workgroup's share `quota` of them
+  const uint32_t G = gridDim.x, pieces = a.K / 64, count = items[blocks];
+  if (count == 0) return;
+  const uint32_t alike = G / count < (uint32_t)a.S ? G / count : a.S;
+  const bool one = 10 * alike * count >= (pieces <= 24 * alike ? 7 : 9) * G;
+  const uint32_t* first = one ? items : loads;
+  const uint32_t span = one ? alike : pieces < 128 ? pieces : 128;
+  const uint32_t all = first[blocks] * span;              // T <= kLoraRows: below 2^32
+  uint32_t quota = 1;
+  if (!one) {
+    // no item has more than a.S parts, and each has a unit at least
+    const uint32_t least = ((RT + MT) * span + a.S - 2) / (a.S - 1), even = (all + G - 1) / G;
+    quota = even > least ? even : least;
+  }
+  // consecutive shares to the workgroups of one XCD (workgroups are dealt to the 8 XCDs in
+  // turn), so that an adapter's A is read through one L2 or two
+  const uint32_t wg = (blockIdx.x & 7) * (G / 8) + blockIdx.x / 8;
+  const uint32_t u0 = wg * quota, u1 = u0 + quota < all ? u0 + quota : all;
+  if (u0 >= all) return;
+  int lo = -1;                            // the block that holds the first item
+  const uint32_t w0 = u0 / span;
+  for (uint32_t b0 = 0; b0 < blocks; b0 += 64)
+    lo += __builtin_popcountll(
+        __builtin_amdgcn_ballot_w64(b0 + lane < blocks && first[b0 + lane] <= w0));
+  int64_t r0 = (int64_t)lo * per * 64;
+  uint32_t begin = __builtin_amdgcn_readfirstlane(first[lo]) * span;   // where the item at hand begins
+  for (; begin < u1; r0 += 64) {
+    const int id = row_id(a, r0 + lane);
+    uint64_t starts = run_starts<M>(a, lane, id);
+    for (; starts && begin < u1; starts &= starts - 1) {
+      const int at = __builtin_ctzll(starts), adapter = __builtin_amdgcn_readlane(id, at);
+      const int tile = at & ~(M - 1);
+      const uint64_t rows = run_rows<M>(id, adapter, at);
+      const uint32_t c = one ? 1 : RT + tiles_of(rows);
+      const uint32_t mine = begin;
+      begin += c * span;
+      if (begin <= u0) continue;
+      const uint32_t x0 = u0 > mine ? (u0 - mine + c - 1) / c : 0, to = (u1 - mine + c - 1) / c;
+      const uint32_t x1 = to < span ? to : span;
+      if (x0 >= x1) continue;
+      const uint32_t head = mine / quota;
+      if (wg == head && tid < 64 && ((rows >> tid) & 1))
+        a.parts[r0 + tid] = (int)((mine + c * (span - 1)) / quota - head) + 1;
+      down_item<MT, RT>(a, r0 + tile, rows >> tile, adapter, (int)(wg - head), (int)(x0 * pieces / span),
+                        (int)(x1 * pieces / span), red);
     }
   }
-  if (t >= a.T) return;
+}
+
+// out = base + h B^T for 16 MT rows and 16 CT columns a wave.  Weights are the MFMA's row
+// operand and the rows of a tile its columns, so that a lane's four results are consecutive
+// output columns; two products over interleaved weights give it eight, one 16-byte load of
+// base (where the products' sum begins) and one store.  h goes in as rounded + rest, RS
+// 32-deep steps each, from LDS, where the workgroup has put it for its rows; an adapter's
+// weights are loaded once for all its rows, those of NB adapters at a time.  Workgroup z = q
+// takes the rows' adapters of its q, and q = 0 the rows without one.
+template <int MT, int RS, int CT, int NB, bool VEC>
+__global__ void __launch_bounds__(64 * kUpWaves)
+lora_up_kernel(LoraArgs a) {
+  constexpr int M = MT * kTile, HW = RS * 64 + 8;         // LDS row: rounded, rest, 16 bytes
+  __shared__ __attribute__((aligned(16))) uint16_t hs[M * HW];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int l16 = lane & 15, g = lane >> 4, q = blockIdx.z;
+  const uint32_t across = (uint32_t)((a.N + kUpWaves * CT * 16 - 1) / (kUpWaves * CT * 16));
+  const uint32_t tile = blockIdx.x / across;             // column blocks of a row tile in turn
+  const int64_t t0 = (int64_t)tile * M;
+  const int64_t n0 = ((int64_t)(blockIdx.x - tile * across) * kUpWaves + wave) * (CT * 16);
+  TileAdapters<M> ad(a, t0, lane, q, a.up_Q);
+  const uint64_t mine = ad.own | (q == 0 ? ad.none : 0);  // rows that this workgroup writes
+  if (!mine) return;
+
+  f32x4 out[MT][CT];
 #pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    const int64_t n = n0 + 32 * p + 8 * g;
-    if (n >= a.N) continue;
+  for (int m = 0; m < MT; ++m) {
+    const int64_t t = t0 + m * kTile + l16;
+    const bool here = (mine >> (m * kTile + l16)) & 1;
+    const uint16_t* base = a.base + t * a.ld_base + n0 + 8 * g;
+#pragma unroll
+    for (int p = 0; p < CT / 2; ++p) {
+      float v[8];
+      uint32_t u[4] = {0, 0, 0, 0};
+      const int64_t n = n0 + 32 * p + 8 * g;
+      if (a.base && here) {
+        if (VEC && n + 8 <= a.N) {
+          const uint4 x = *(const uint4*)(base + 32 * p);
+          u[0] = x.x; u[1] = x.y; u[2] = x.z; u[3] = x.w;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (n + e < a.N) u[e / 2] |= (uint32_t)base[32 * p + e] << (16 * (e & 1));
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[2 * e] = from_bf16(u[e] & 0xFFFFu);
+        v[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
+      }
+      out[m][2 * p] = f32x4{v[0], v[1], v[2], v[3]};
+      out[m][2 * p + 1] = f32x4{v[4], v[5], v[6], v[7]};
+    }
+  }
+  // weight rows of this lane: MFMA row m of product c is column 32 (c / 2) + 8 (m / 4) +
+  // 4 (c % 2) + m % 4, so that result j of lane group g is column 32 (c / 2) + 8 g + 4 (c % 2) + j
+  uint32_t brow[CT];                         // bytes from the adapter's B: below 2^31
+#pragma unroll
+  for (int c = 0; c < CT; ++c) {
+    const int64_t n = n0 + 32 * (c / 2) + 8 * (l16 / 4) + 4 * (c & 1) + (l16 & 3);
+    brow[c] = (uint32_t)(n < a.N ? n : a.N - 1) * (uint32_t)(a.R * 2);
+  }
+  uint32_t piece[RS];                        // this lane's 8 ranks of a step, within R
+#pragma unroll
+  for (int st = 0; st < RS; ++st) piece[st] = (4 * st + g) * 8 < a.R ? (4 * st + g) * 8 : 0;
+
+  int adapter[NB];
+  uint64_t rows[NB];
+  uint4 w[NB][CT][RS];
+  bool more = n0 < a.N;
+  auto load_weights = [&]() {
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+      more = more && ad.next(&adapter[k], &rows[k]);
+      if (!more) {
+        rows[k] = 0;
+        continue;
+      }
+      const uint8_t* B = (const uint8_t*)(a.B + (int64_t)adapter[k] * a.N * a.R);
+#pragma unroll
+      for (int c = 0; c < CT; ++c)
+#pragma unroll
+        for (int st = 0; st < RS; ++st)
+          w[k][c][st] = *(const uint4*)(B + (brow[c] + 2 * piece[st]));
+    }
+  };
+  load_weights();
+
+  // h of the rows, 8 ranks an item
+  for (int i = tid; i < M * RS * 4; i += 64 * kUpWaves) {
+    const int row = i / (RS * 4), c = (i % (RS * 4)) * 8;
     float v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = out[2 * p + i / 4][i & 3];
-    if (VEC && n + 8 <= a.N) {
-      uint32_t w[4] = {0, 0, 0, 0};
-      if (a.base) {
-        const uint4 u = *(const uint4*)(a.base + t * a.ld_base + n);
-        w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
-      }
+    for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+    if (((ad.own >> row) & 1) && c < a.R) {
+      const float* p = a.h + (t0 + row) * a.R + c;
+      const int S = a.parts ? a.parts[t0 + row] : a.S;
+      for (int s0 = 0; s0 < S; s0 += 4) {
+        float4 x[4], y[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float lo = v[2 * i] + from_bf16(w[i] & 0xFFFFu);
-        const float hi = v[2 * i + 1] + __uint_as_float(w[i] & 0xFFFF0000u);
-        w[i] = round_bf16(lo) | (round_bf16(hi) << 16);
-      }
-      *(uint4*)(a.out + t * a.ld_out + n) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (n + i < a.N) {
-          const float b = a.base ? from_bf16(a.base[t * a.ld_base + n + i]) : 0.0f;
-          a.out[t * a.ld_out + n + i] = (uint16_t)round_bf16(v[i] + b);
+        for (int s = 0; s < 4; ++s) {
+          const float* ps = p + (s0 + s < S ? s0 + s : S - 1) * a.h_part;
+          x[s] = *(const float4*)ps;
+          y[s] = *(const float4*)(ps + 4);
         }
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+          if (s0 + s < S) {
+            v[0] += x[s].x; v[1] += x[s].y; v[2] += x[s].z; v[3] += x[s].w;
+            v[4] += y[s].x; v[5] += y[s].y; v[6] += y[s].z; v[7] += y[s].w;
+          }
+      }
+    }
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      hi[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+      // the rest of an infinity (NaN) becomes a number that does not matter beside it
+      const float r0 = v[2 * e] - from_bf16(hi[e] & 0xFFFFu);
+      const float r1 = v[2 * e + 1] - __uint_as_float(hi[e] & 0xFFFF0000u);
+      lo[e] = pack_bf16(__builtin_amdgcn_fmed3f(r0, -0x1p120f, 0x1p120f),
+                        __builtin_amdgcn_fmed3f(r1, -0x1p120f, 0x1p120f));
+    }
+    *(uint4*)(hs + row * HW + c) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *(uint4*)(hs + row * HW + RS * 32 + c) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  }
+  __syncthreads();
+
+  if (n0 >= a.N) return;
+  for (; rows[0]; load_weights()) {
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+      if (!rows[k]) break;
+      const int rank = rank_of(a, adapter[k]);
+      if (rank < a.R) {                      // what lies past the adapter's rank is not its
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+          for (int st = 0; st < RS; ++st) {
+            uint32_t x[4] = {w[k][c][st].x, w[k][c][st].y, w[k][c][st].z, w[k][c][st].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int r = (int)piece[st] + 2 * e;
+              x[e] = r >= rank ? 0u : r + 1 >= rank ? x[e] & 0xFFFFu : x[e];
+            }
+            w[k][c][st] = make_uint4(x[0], x[1], x[2], x[3]);
+          }
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const uint32_t r16 = (uint32_t)(rows[k] >> (m * kTile)) & 0xFFFFu;
+        if (!r16) continue;
+        uint4 hi[RS], lo[RS];
+#pragma unroll
+        for (int st = 0; st < RS; ++st) {
+          const uint16_t* p = hs + (m * kTile + l16) * HW + (4 * st + g) * 8;
+          hi[st] = *(const uint4*)p;
+          lo[st] = *(const uint4*)(p + RS * 32);
+        }
+        const bool here = (r16 >> l16) & 1;
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+          f32x4 acc = out[m][c];
+#pragma unroll
+          for (int st = 0; st < RS; ++st) {
+            acc = mfma(w[k][c][st], lo[st], acc);
+            acc = mfma(w[k][c][st], hi[st], acc);
+          }
+          if (here) out[m][c] = acc;
+        }
+      }
     }
   }
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    if (!((mine >> (m * kTile + l16)) & 1)) continue;
+    uint16_t* o = a.out + (t0 + m * kTile + l16) * a.ld_out + n0 + 8 * g;
+#pragma unroll
+    for (int p = 0; p < CT / 2; ++p) {
+      const int64_t n = n0 + 32 * p + 8 * g;
+      const f32x4 x = out[m][2 * p], y = out[m][2 * p + 1];
+      const uint32_t u[4] = {pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(y[0], y[1]),
+                             pack_bf16(y[2], y[3])};
+      if (VEC && n + 8 <= a.N) {
+        *(uint4*)(o + 32 * p) = make_uint4(u[0], u[1], u[2], u[3]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (n + e < a.N) o[32 * p + e] = (uint16_t)(u[e / 2] >> (16 * (e & 1)));
+      }
+    }
+  }
+}
+
+template <int MT>
+void launch_down(const LoraArgs& a, hipStream_t stream) {
+  const dim3 grid(a.grid), block(64 * kDownWaves);
+  if (a.R <= 16) hipLaunchKernelGGL((lora_down_kernel<MT, 1>), grid, block, 0, stream, a);
+  else if (a.R <= 32) hipLaunchKernelGGL((lora_down_kernel<MT, 2>), grid, block, 0, stream, a);
+  else if (a.R <= 64) hipLaunchKernelGGL((lora_down_kernel<MT, 4>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((lora_down_kernel<MT == 4 ? 2 : MT, 8>), grid, block, 0, stream, a);
+}
+
+void launch_down_rows(const LoraArgs& a, hipStream_t stream) {
+  const dim3 grid((unsigned)a.T, a.S), block(64 * kDownWaves);
+  if (a.R <= 16) hipLaunchKernelGGL((lora_down_rows_kernel<1>), grid, block, 0, stream, a);
+  else if (a.R <= 32) hipLaunchKernelGGL((lora_down_rows_kernel<2>), grid, block, 0, stream, a);
+  else if (a.R <= 64) hipLaunchKernelGGL((lora_down_rows_kernel<4>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((lora_down_rows_kernel<8>), grid, block, 0, stream, a);
+}
+
+template <int MT, int RS, int CT, int NB>
+void launch_up(const LoraArgs& a, hipStream_t stream) {
+  const int64_t rows = MT * kTile, cols = kUpWaves * CT * 16;
+  const dim3 grid((unsigned)((a.T + rows - 1) / rows * ((a.N + cols - 1) / cols)), 1, a.up_Q);
+  const bool vec = (((uintptr_t)a.out | (uintptr_t)a.base) & 15) == 0 && a.ld_out % 8 == 0 &&
+                   (!a.base || a.ld_base % 8 == 0);
+  if (vec)
+    hipLaunchKernelGGL((lora_up_kernel<MT, RS, CT, NB, true>), grid, dim3(64 * kUpWaves), 0, stream, a);
+  else
+    hipLaunchKernelGGL((lora_up_kernel<MT, RS, CT, NB, false>), grid, dim3(64 * kUpWaves), 0, stream, a);
 }
 
 }  // namespace
 
-void lora_split(int64_t T, int64_t K, int64_t R, int* S, int* Q) {
-  (void)R;
-  const int64_t tiles = (T + kTile - 1) / kTile, deep = (int64_t)kDownWaves * kFrags * 32;
-  int64_t s = (K + deep - 1) / deep;                       // what the registers need
-  int64_t q = 1;
-  while (q < kTile && tiles * s * q < 512 && q < T) q *= 2;
-  while (tiles * s * q < 512 && K / s > 1024) ++s;
-  *S = (int)s;
-  *Q = (int)q;
+void lora_plan(LoraArgs* a) {
+  const int64_t T = a->T, K = a->K;
+  auto cdiv = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
+  // first kernel
+  const int64_t most = K >= 512 ? K / 512 : 1;             // parts: a piece a wave at least
+  if (T <= kLoraFewRows) {
+    a->mt = 0;
+    const int64_t S = cdiv(256, T);
+    a->S = (int)(S < most ? S : most);
+  } else {
+    const int64_t rows = T < kLoraRows ? T : kLoraRows;
+    int mt = a->R <= 64 ? 4 : 2;
+    while (mt > 1 && cdiv(rows, mt * kTile) * most < 256) mt /= 2;
+    const int64_t S = cdiv(256, cdiv(rows, mt * kTile)) + 1;
+    a->mt = mt;
+    a->S = (int)(S < most ? S : most < 2 ? 2 : most);
+    a->grid = 256;
+  }
+  // second kernel
+  a->up_mt = T <= 16 ? 1 : 4;
+  const int64_t up_tiles = cdiv(T, a->up_mt * kTile) * cdiv(a->N, a->up_mt == 1 ? 128 : 256);
+  int Q = 1;
+  while (Q < 16 && Q < T && 2 * Q * up_tiles <= 512) Q *= 2;
+  a->up_Q = Q;
+  a->h_part = T * a->R;
 }
 
-void launch_lora(const LoraArgs& a, hipStream_t stream) {
-  const unsigned tiles = (unsigned)((a.T + kTile - 1) / kTile);
-  const int rt = (a.R + 15) / 16, steps = (2 * (a.R / 8) + 3) / 4;
-  hipLaunchKernelGGL(lora_down_kernel, dim3(tiles, a.S, a.Q), dim3(64 * kDownWaves),
-                     (size_t)kDownWaves * rt * 256 * 4, stream, a);
-  const unsigned cols = (unsigned)((a.N + kUpWaves * kUpCols - 1) / (kUpWaves * kUpCols));
-  const size_t lds = (size_t)kTile * (steps * 32 + 8) * 2;
-  const bool vec = (((uintptr_t)a.out | (uintptr_t)a.base) & 15) == 0 && a.ld_out % 8 == 0 &&
-                   (!a.base || a.ld_base % 8 == 0);
-  if (vec)
-    hipLaunchKernelGGL((lora_up_kernel<true>), dim3(tiles, cols), dim3(64 * kUpWaves), lds, stream, a);
-  else
-    hipLaunchKernelGGL((lora_up_kernel<false>), dim3(tiles, cols), dim3(64 * kUpWaves), lds, stream, a);
+void launch_lora(const LoraArgs& all, hipStream_t stream) {
+  for (int64_t t = 0; t < all.T; t += kLoraRows) {
+    LoraArgs a = all;
+    a.T = all.T - t < kLoraRows ? all.T - t : kLoraRows;
+    a.x += t * a.ldx;
+    a.ids += t;
+    if (a.base) a.base += t * a.ld_base;
+    a.out += t * a.ld_out;
+    a.h += t * a.R;
+    if (a.parts) a.parts += t;
+    if (a.mt == 0) launch_down_rows(a, stream);
+    else if (a.mt == 4) launch_down<4>(a, stream);
+    else if (a.mt == 2) launch_down<2>(a, stream);
+    else launch_down<1>(a, stream);
+    if (a.up_mt == 1) {
+      if (a.R <= 32) launch_up<1, 1, 2, 4>(a, stream);
+      else if (a.R <= 64) launch_up<1, 2, 2, 2>(a, stream);
+      else launch_up<1, 4, 2, 1>(a, stream);
+    } else {
+      if (a.R <= 32) launch_up<4, 1, 4, 2>(a, stream);
+      else if (a.R <= 64) launch_up<4, 2, 4, 1>(a, stream);
+      else launch_up<4, 4, 4, 1>(a, stream);
+    }
+  }
 }
 
 }  // namespace dg

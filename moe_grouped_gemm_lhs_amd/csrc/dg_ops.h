@@ -50,7 +50,8 @@ void launch_route_backward(const RouteArgs& a, hipStream_t stream);
 
 // Low-rank adapters (defined in dg_lora.hip).
 constexpr int kLoraMaxR = 128;
-constexpr int kLoraDownFrags = 16;   // 32-deep pieces of K in a wave's registers
+constexpr int64_t kLoraFewRows = 128;
+constexpr int64_t kLoraRows = (int64_t)1 << 20;   // rows of a launch
 
 struct LoraArgs {
   const uint16_t* x;
@@ -64,14 +65,20 @@ struct LoraArgs {
   int64_t ld_base;
   uint16_t* out;
   int64_t ld_out;
-  float* h;                    // S x T x R, in the workspace
+  float* h;                    // S x T x R, the workspace
+  int64_t h_part;              // elements from one part to the next
+  int* parts;                  // T, behind it: parts of a row's sums (nullptr: S)
   int64_t T, N;
   int K, R, L;
-  int S, Q;                    // shares of K, workgroups that share a tile's adapters
+  // the plan for the sizes (lora_plan)
+  int mt;                      // first kernel: row tiles of 16 a workgroup; 0: for few rows
+  int S;                       // parts of the sums over K, at most
+  int grid;                    // workgroups of the kernel for many rows
+  int up_mt;                   // second kernel: row tiles of 16 a workgroup
+  int up_Q;                    // workgroups over the adapters of the same rows
 };
 
-// Shares of K and workgroups over a tile's adapters for these sizes.
-void lora_split(int64_t T, int64_t K, int64_t R, int* S, int* Q);
+void lora_plan(LoraArgs* a);
 void launch_lora(const LoraArgs& a, hipStream_t stream);
 
 }  // namespace dg

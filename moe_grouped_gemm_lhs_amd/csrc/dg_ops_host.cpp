@@ -54,7 +54,7 @@ int route_vec(const void* p, int64_t E, int64_t ld, int bf16) {
 
 bool lora_shape(int64_t T, int64_t N, int64_t K, int64_t R, int64_t L) {
   // K % 128 as for the projection beside which the adapters stand
-  return T >= 0 && T <= INT32_MAX - 64 && N >= 0 && N <= INT32_MAX - 1024 && K > 0 &&
+  return T >= 0 && T <= INT32_MAX - 64 && N >= 0 && N <= ((int64_t)1 << 22) && K > 0 &&
          K % dg::kBlockK == 0 && K <= ((int64_t)1 << 22) && R >= 8 && R <= dg::kLoraMaxR &&
          R % 8 == 0 && L >= 1 && L <= INT32_MAX;
 }
@@ -127,9 +127,10 @@ dg_status dg_moe_route_backward(const void* logits, int dtype, int64_t ld, const
 
 size_t dg_lora_workspace_bytes(int64_t T, int64_t N, int64_t K, int64_t R, int64_t L) {
   if (!lora_shape(T, N, K, R, L) || T == 0 || N == 0) return 0;
-  int S = 0, Q = 0;
-  dg::lora_split(T, K, R, &S, &Q);
-  return (size_t)S * T * R * 4;
+  dg::LoraArgs a{};
+  a.T = T; a.N = N; a.K = (int)K; a.R = (int)R;
+  dg::lora_plan(&a);
+  return (size_t)a.S * T * R * 4 + (a.mt > 0 ? (size_t)T * 4 : 0);
 }
 
 dg_status dg_lora_bf16(const uint16_t* X, int64_t ldx, const uint16_t* A, const uint16_t* B,
@@ -157,7 +158,8 @@ dg_status dg_lora_bf16(const uint16_t* X, int64_t ldx, const uint16_t* A, const 
   a.base = base; a.ld_base = ld_base; a.out = out; a.ld_out = ld_out;
   a.h = (float*)workspace;
   a.T = T; a.N = N; a.K = (int)K; a.R = (int)R; a.L = (int)L;
-  dg::lora_split(T, K, R, &a.S, &a.Q);
+  dg::lora_plan(&a);
+  if (a.mt > 0) a.parts = (int*)(a.h + (int64_t)a.S * T * R);
   (void)hipGetLastError();
   dg::launch_lora(a, (hipStream_t)stream);
   return hipGetLastError() == hipSuccess ? DG_OK : DG_ERR_HIP;

@@ -123,6 +123,43 @@ def test_many_rows_of_rank_64():
     check(make(2100, 520, 128, 64, 4, 3), ids_of(2100, 4, "segments"))
 
 
+@pytest.mark.parametrize("T,K,rank,L", [(2000, 4096, 64, 9), (1500, 2048, 128, 5), (700, 8192, 16, 40),
+                                        (4100, 1024, 32, 70), (130, 128, 8, 3), (3000, 1152, 72, 300)])
+def test_parts_of_long_batches(T, K, rank, L):
+    """Prompts whose ends fall inside tiles, then single rows: items cut into parts of K, even
+    and uneven ones."""
+    p = make(T, 40, K, rank, L, T + K)
+    rng = np.random.default_rng(T)
+    prompts = np.sort(rng.integers(0, max(L // 3, 1), T - min(L, T // 4)))
+    ids = np.concatenate([prompts, np.arange(min(L, T // 4))])
+    check(p, ids, what="prompts and single rows")
+    ids[rng.random(T) < 0.8] = -1                # few items
+    check(p, ids, what="mostly without an adapter")
+
+
+def test_one_row_with_an_adapter_among_many():
+    p = make(1000, 24, 1024, 16, 3, 21)
+    ids = np.full(1000, -1)
+    ids[777] = 2
+    check(p, ids)
+
+
+def test_more_rows_than_a_launch_takes():
+    T, K, N, rank, L = (1 << 20) + 77, 128, 8, 8, 3
+    p = make(1, N, K, rank, L, 22)
+    x = torch.randn(T, K, device=DEV, dtype=torch.float32).to(BF)
+    base = torch.randn(T, N, device=DEV, dtype=torch.float32).to(BF)
+    ids = ((torch.arange(T, device=DEV) // 1000) % (L + 1) - 1).int()
+    got = dg.dg_lora_bf16(x, p["A"].to(DEV), p["B"].to(DEV), ids, base)
+    torch.cuda.synchronize()
+    rows = np.concatenate([np.arange(300), np.arange((1 << 20) - 200, T)])
+    ref, size = R.lora(host(x[rows]), host(p["A"]), host(p["B"]), ids.cpu().numpy()[rows], None, None,
+                       host(base[rows]))
+    assert np.all(np.abs(host(got[rows]) - ref) <= R.lora_tolerance(ref, size, K))
+    none = ids < 0
+    assert torch.equal(got[none], base[none])
+
+
 def test_no_scales_no_base():
     p = make(30, 100, 256, 16, 4, 5)
     check(p, ids_of(30, 4, "mixed"), scales=False)

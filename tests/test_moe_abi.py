@@ -75,7 +75,7 @@ def lora(lib, X=A16, ldx=512, A=A16, B=A16, ids=A4, scales=None, ranks=None, bas
 
 def test_lora_codes(lib):
     for bad in (dict(K=500, ldx=504), dict(K=0), dict(R=4), dict(R=12), dict(R=136), dict(L=0), dict(T=-1),
-                dict(N=-1), dict(ldx=508), dict(ldx=504), dict(ldo=255), dict(base=A16, ldb=255),
+                dict(N=-1), dict(N=(1 << 22) + 1, ldo=1 << 23), dict(ldx=508), dict(ldx=504), dict(ldo=255), dict(base=A16, ldb=255),
                 dict(base=A16, ldb=264, out=A16), dict(T=1 << 31), dict(K=1 << 23, ldx=1 << 23)):
         assert lora(lib, **bad) == 2, bad
     assert lora(lib, T=0, X=None, ws=None) == 0
