@@ -257,8 +257,8 @@ dg_status dg_transpose_fp8(const uint8_t *X, uint8_t *Y, int64_t rows, int64_t c
  * need counts.  Pointers need their element's alignment only (rows that start on 16 bytes,
  * 8 for bf16, with E and ld multiples of 4, are read in wider loads).
  *
- * With counts the call needs a workspace of dg_moe_route_workspace_bytes bytes, 16-byte
- * aligned.  It may hold anything before and after the call, so one buffer can serve this
+ * With counts the call needs a workspace of dg_moe_route_workspace_bytes bytes (0 for a few
+ * rows: none), 16-byte aligned.  It may hold anything before and after the call, so one buffer can serve this
  * call and dg_lora_bf16 in stream order (not two calls that may overlap, and not the GEMM
  * calls, which need theirs zero).
  *

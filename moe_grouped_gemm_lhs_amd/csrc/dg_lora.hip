@@ -41,9 +41,40 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)lo, (__bf16)hi});
 }
 
-// The adapters that M <= 64 rows from t0 name, those with id = q modulo Q (a power of two)
-// only: lane l holds the id of row l % M (-1: none).  next() gives them one by one, in the
-// order of their first rows, with the rows that are theirs.
+// Eight bf16 numbers at any element: one 16-byte access (the hardware takes those at any
+// address).
+__device__ __forceinline__ uint4 load8(const uint16_t* p) {
+  uint4 v;
+  __builtin_memcpy(&v, p, 16);
+  return v;
+}
+__device__ __forceinline__ void store8(uint16_t* p, const uint4& v) { __builtin_memcpy(p, &v, 16); }
+
+// Lanes eight apart trade: the lower one's y for the upper one's x.  Its own inverse.
+__device__ __forceinline__ void trade(uint4& x, uint4& y, bool upper) {
+  uint32_t a[4] = {x.x, x.y, x.z, x.w}, b[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int got = __builtin_amdgcn_mov_dpp((int)(upper ? a[i] : b[i]), 0x128, 0xF, 0xF, true);
+    a[i] = upper ? (uint32_t)got : a[i];
+    b[i] = upper ? b[i] : (uint32_t)got;
+  }
+  x = make_uint4(a[0], a[1], a[2], a[3]);
+  y = make_uint4(b[0], b[1], b[2], b[3]);
+}
+
+// A number as the sum of two bf16 numbers, itself rounded (low half) and the rest rounded.
+__device__ __forceinline__ uint32_t split_bf16(float v) {
+  const uint32_t hi = pack_bf16(v, 0.0f) & 0xFFFFu;
+  // the rest of an infinity (NaN) becomes a number that does not matter beside it
+  const float rest = __builtin_amdgcn_fmed3f(v - from_bf16(hi), -0x1p120f, 0x1p120f);
+  return hi | (pack_bf16(0.0f, rest) & 0xFFFF0000u);
+}
+
+// The adapters that M <= 64 rows from t0 name: lane l holds the id of row l % M (-1: none).
+// Of Q workgroups (a power of two) on the same rows the q-th has those with id = q modulo Q
+// if there are many, and q = 0 all of them where the rows are one or two runs.  next() gives
+// its adapters one by one, in the order of their first rows, with the rows that are theirs.
 template <int M>
 struct TileAdapters {
   static constexpr uint64_t kRows = M == 64 ? ~0ull : (1ull << (M & 63)) - 1;
@@ -54,8 +85,14 @@ struct TileAdapters {
     const int64_t t = t0 + (lane & (M - 1));
     const int i = t < a.T ? a.ids[t] : -1;
     id = i >= 0 && i < a.L ? i : -1;
-    own = left = __builtin_amdgcn_ballot_w64(id >= 0 && (id & (Q - 1)) == q) & kRows;
+    own = __builtin_amdgcn_ballot_w64(id >= 0) & kRows;
     none = __builtin_amdgcn_ballot_w64(id < 0 && t < a.T) & kRows;
+    if (Q > 1) {
+      const uint64_t ends = __builtin_amdgcn_ballot_w64(id != __shfl_down(id, 1, 64)) & (kRows >> 1);
+      if (__builtin_popcountll(ends) <= 1) own = q == 0 ? own : 0;
+      else own &= __builtin_amdgcn_ballot_w64((id & (Q - 1)) == q);
+    }
+    left = own;
   }
   __device__ __forceinline__ bool next(int* adapter, uint64_t* rows) {
     if (!left) return false;
@@ -77,11 +114,10 @@ __device__ __forceinline__ int rank_of(const LoraArgs& a, int adapter) {
 // consecutive bytes of a piece, half for each instruction (x and A alike, so that the
 // products pair up), and the four lane groups a 128-byte line.  U pieces are in flight
 // while the ones before them are multiplied.
-template <int NA, int RT>
+template <int U, int NA, int RT>
 __device__ __forceinline__ void down_products(const uint16_t* const (&xp)[NA],
                                               const uint16_t* const (&ap)[RT], int nf,
                                               f32x4 (&acc)[NA][RT]) {
-  constexpr int U = NA + RT <= 2 ? 4 : NA + RT <= 4 ? 2 : 1;
   uint4 x[2][U][NA][2], w[2][U][RT][2];
   // pieces past the last repeat it and are not multiplied
   auto load = [&](int b, int f) {
@@ -137,7 +173,7 @@ __device__ __forceinline__ void down_tiles(const LoraArgs& a, int64_t t0, uint64
 #pragma unroll
     for (int r = 0; r < RT; ++r) sum[m][r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
-  down_products<NA, RT>(xp, ap, nf, sum);
+  down_products<(NA + RT <= 2 ? 4 : NA + RT <= 4 ? 2 : 1)>(xp, ap, nf, sum);
 #pragma unroll
   for (int m = 0; m < NA; ++m)
 #pragma unroll
@@ -243,7 +279,8 @@ lora_down_rows_kernel(LoraArgs a) {
 // Many rows: an item is a run of rows of one adapter within a tile of 16 MT.  Every workgroup
 // counts the items for itself from the ids (64 rows a ballot), without a launch to plan it,
 // and then knows its share of them:
-//  - where dividing each item's K alike gives most workgroups one part, it takes that part;
+//  - where dividing each item's K alike gives most workgroups one part (or each item as many
+//    as it may have), it takes that part;
 //  - otherwise the items' pieces of K, one item after the other, are dealt out evenly.  A
 //    piece is counted as its loads, RT for the adapter's ranks and one for each tile of 16
 //    that the run touches, so the single rows of a mixed batch and the ends of prompts
@@ -332,7 +369,7 @@ lora_down_kernel(LoraArgs a) {
   const uint32_t G = gridDim.x, pieces = a.K / 64, count = items[blocks];
   if (count == 0) return;
   const uint32_t alike = G / count < (uint32_t)a.S ? G / count : a.S;
-  const bool one = 10 * alike * count >= (pieces <= 24 * alike ? 7 : 9) * G;
+  const bool one = alike == (uint32_t)a.S || 10 * alike * count >= (pieces <= 24 * alike ? 7 : 9) * G;
   const uint32_t* first = one ? items : loads;
   const uint32_t span = one ? alike : pieces < 128 ? pieces : 128;
   const uint32_t all = first[blocks] * span;              // T <= kLoraRows: below 2^32
@@ -380,59 +417,65 @@ lora_down_kernel(LoraArgs a) {
 // out = base + h B^T for 16 MT rows and 16 CT columns a wave.  Weights are the MFMA's row
 // operand and the rows of a tile its columns, so that a lane's four results are consecutive
 // output columns; two products over interleaved weights give it eight, one 16-byte load of
-// base (where the products' sum begins) and one store.  h goes in as rounded + rest, RS
-// 32-deep steps each, from LDS, where the workgroup has put it for its rows; an adapter's
-// weights are loaded once for all its rows, those of NB adapters at a time.  Workgroup z = q
-// takes the rows' adapters of its q, and q = 0 the rows without one.
-template <int MT, int RS, int CT, int NB, bool VEC>
-__global__ void __launch_bounds__(64 * kUpWaves)
+// base (where the products' sum begins) and one store, whatever the rows' alignment.  Two
+// such accesses of a lane cover 64 bytes of 16 rows each; lanes eight apart trade one of
+// them, so that an access covers 128 bytes of 8 rows (a copy by rows of 64 bytes runs at 3.4
+// TB/s here, by 128 at 3.95; 4096 x 7168).  h goes in as rounded + rest, RS 32-deep steps each, from LDS, where the workgroup has put
+// it for its rows; an adapter's weights are loaded once for all its rows, those of NB
+// adapters at a time.  Workgroup z = q takes the rows' adapters of its q, and q = 0 the rows
+// without one.
+template <int MT, int RS, int CT, int NB>
+__global__ void __launch_bounds__(64 * kUpWaves, RS <= 2 ? 3 : 2)
 lora_up_kernel(LoraArgs a) {
   constexpr int M = MT * kTile, HW = RS * 64 + 8;         // LDS row: rounded, rest, 16 bytes
+  constexpr int W = kUpWaves, C = CT * 16;
   __shared__ __attribute__((aligned(16))) uint16_t hs[M * HW];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, g = lane >> 4, q = blockIdx.z;
-  const uint32_t across = (uint32_t)((a.N + kUpWaves * CT * 16 - 1) / (kUpWaves * CT * 16));
-  const uint32_t tile = blockIdx.x / across;             // column blocks of a row tile in turn
+  const uint32_t across = (uint32_t)((a.N + W * C - 1) / (W * C));
+  // column blocks of a row tile in turn; the last rows first, where a mixed batch has its
+  // single rows and the work of a tile is longest
+  const uint32_t back = blockIdx.x / across, tile = gridDim.x / across - 1 - back;
   const int64_t t0 = (int64_t)tile * M;
-  const int64_t n0 = ((int64_t)(blockIdx.x - tile * across) * kUpWaves + wave) * (CT * 16);
+  const int64_t n0 = ((int64_t)(blockIdx.x - back * across) * W + wave) * C;
   TileAdapters<M> ad(a, t0, lane, q, a.up_Q);
   const uint64_t mine = ad.own | (q == 0 ? ad.none : 0);  // rows that this workgroup writes
   if (!mine) return;
 
-  f32x4 out[MT][CT];
+  // A lane's 16-byte accesses to the rows of a tile: the i-th of pair p, two pairs together
+  // where there are two (see above).  at(): row in the tile and column.
+  constexpr bool kTrade = CT % 4 == 0;
+  auto at = [&](int p, int* col) {
+    *col = kTrade ? 64 * (p / 2) + 32 * (l16 >> 3) + 8 * g : 32 * p + 8 * g;
+    return kTrade ? (l16 & 7) + 8 * (p & 1) : l16;
+  };
+  uint4 base[MT][CT / 2];
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
-    const int64_t t = t0 + m * kTile + l16;
-    const bool here = (mine >> (m * kTile + l16)) & 1;
-    const uint16_t* base = a.base + t * a.ld_base + n0 + 8 * g;
 #pragma unroll
     for (int p = 0; p < CT / 2; ++p) {
-      float v[8];
-      uint32_t u[4] = {0, 0, 0, 0};
-      const int64_t n = n0 + 32 * p + 8 * g;
-      if (a.base && here) {
-        if (VEC && n + 8 <= a.N) {
-          const uint4 x = *(const uint4*)(base + 32 * p);
-          u[0] = x.x; u[1] = x.y; u[2] = x.z; u[3] = x.w;
+      int col;
+      const int row = m * kTile + at(p, &col);
+      const int64_t n = n0 + col;
+      const uint16_t* b = a.base + (t0 + row) * a.ld_base + n;
+      base[m][p] = make_uint4(0, 0, 0, 0);
+      if (a.base && ((mine >> row) & 1)) {
+        if (n + 8 <= a.N) {
+          base[m][p] = load8(b);
         } else {
+          uint32_t u[4] = {0, 0, 0, 0};
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            if (n + e < a.N) u[e / 2] |= (uint32_t)base[32 * p + e] << (16 * (e & 1));
+            if (n + e < a.N) u[e / 2] |= (uint32_t)b[e] << (16 * (e & 1));
+          base[m][p] = make_uint4(u[0], u[1], u[2], u[3]);
         }
       }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[2 * e] = from_bf16(u[e] & 0xFFFFu);
-        v[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
-      }
-      out[m][2 * p] = f32x4{v[0], v[1], v[2], v[3]};
-      out[m][2 * p + 1] = f32x4{v[4], v[5], v[6], v[7]};
     }
   }
   // weight rows of this lane: MFMA row m of product c is column 32 (c / 2) + 8 (m / 4) +
   // 4 (c % 2) + m % 4, so that result j of lane group g is column 32 (c / 2) + 8 g + 4 (c % 2) + j
-  uint32_t brow[CT];                         // bytes from the adapter's B: below 2^31
+  uint32_t brow[CT];                         // bytes from the adapter's B: at most 2^30
 #pragma unroll
   for (int c = 0; c < CT; ++c) {
     const int64_t n = n0 + 32 * (c / 2) + 8 * (l16 / 4) + 4 * (c & 1) + (l16 & 3);
@@ -465,7 +508,7 @@ lora_up_kernel(LoraArgs a) {
   load_weights();
 
   // h of the rows, 8 ranks an item
-  for (int i = tid; i < M * RS * 4; i += 64 * kUpWaves) {
+  for (int i = tid; i < M * RS * 4; i += 64 * W) {
     const int row = i / (RS * 4), c = (i % (RS * 4)) * 8;
     float v[8];
 #pragma unroll
@@ -489,22 +532,32 @@ lora_up_kernel(LoraArgs a) {
           }
       }
     }
-    uint32_t hi[4], lo[4];
+    uint32_t h[8];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      hi[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
-      // the rest of an infinity (NaN) becomes a number that does not matter beside it
-      const float r0 = v[2 * e] - from_bf16(hi[e] & 0xFFFFu);
-      const float r1 = v[2 * e + 1] - __uint_as_float(hi[e] & 0xFFFF0000u);
-      lo[e] = pack_bf16(__builtin_amdgcn_fmed3f(r0, -0x1p120f, 0x1p120f),
-                        __builtin_amdgcn_fmed3f(r1, -0x1p120f, 0x1p120f));
-    }
-    *(uint4*)(hs + row * HW + c) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    *(uint4*)(hs + row * HW + RS * 32 + c) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    for (int e = 0; e < 8; ++e) h[e] = split_bf16(v[e]);
+    *(uint4*)(hs + row * HW + c) =
+        make_uint4((h[0] & 0xFFFFu) | (h[1] << 16), (h[2] & 0xFFFFu) | (h[3] << 16),
+                   (h[4] & 0xFFFFu) | (h[5] << 16), (h[6] & 0xFFFFu) | (h[7] << 16));
+    *(uint4*)(hs + row * HW + RS * 32 + c) =
+        make_uint4((h[0] >> 16) | (h[1] & 0xFFFF0000u), (h[2] >> 16) | (h[3] & 0xFFFF0000u),
+                   (h[4] >> 16) | (h[5] & 0xFFFF0000u), (h[6] >> 16) | (h[7] & 0xFFFF0000u));
   }
   __syncthreads();
-
   if (n0 >= a.N) return;
+
+  f32x4 out[MT][CT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+#pragma unroll
+    for (int p = 0; kTrade && p < CT / 2; p += 2) trade(base[m][p], base[m][p + 1], l16 >> 3);
+#pragma unroll
+    for (int c = 0; c < CT; ++c) {
+      const uint4 b = base[m][c / 2];
+      const uint32_t u0 = c & 1 ? b.z : b.x, u1 = c & 1 ? b.w : b.y;
+      out[m][c] = f32x4{from_bf16(u0 & 0xFFFFu), __uint_as_float(u0 & 0xFFFF0000u),
+                        from_bf16(u1 & 0xFFFFu), __uint_as_float(u1 & 0xFFFF0000u)};
+    }
+  }
   for (; rows[0]; load_weights()) {
 #pragma unroll
     for (int k = 0; k < NB; ++k) {
@@ -551,20 +604,29 @@ lora_up_kernel(LoraArgs a) {
   }
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
-    if (!((mine >> (m * kTile + l16)) & 1)) continue;
-    uint16_t* o = a.out + (t0 + m * kTile + l16) * a.ld_out + n0 + 8 * g;
+    uint4 u[CT / 2];
 #pragma unroll
     for (int p = 0; p < CT / 2; ++p) {
-      const int64_t n = n0 + 32 * p + 8 * g;
       const f32x4 x = out[m][2 * p], y = out[m][2 * p + 1];
-      const uint32_t u[4] = {pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(y[0], y[1]),
-                             pack_bf16(y[2], y[3])};
-      if (VEC && n + 8 <= a.N) {
-        *(uint4*)(o + 32 * p) = make_uint4(u[0], u[1], u[2], u[3]);
+      u[p] = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(y[0], y[1]),
+                        pack_bf16(y[2], y[3]));
+    }
+#pragma unroll
+    for (int p = 0; kTrade && p < CT / 2; p += 2) trade(u[p], u[p + 1], l16 >> 3);
+#pragma unroll
+    for (int p = 0; p < CT / 2; ++p) {
+      int col;
+      const int row = m * kTile + at(p, &col);
+      const int64_t n = n0 + col;
+      if (!((mine >> row) & 1)) continue;
+      uint16_t* o = a.out + (t0 + row) * a.ld_out + n;
+      if (n + 8 <= a.N) {
+        store8(o, u[p]);
       } else {
+        const uint32_t x[4] = {u[p].x, u[p].y, u[p].z, u[p].w};
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          if (n + e < a.N) o[32 * p + e] = (uint16_t)(u[e / 2] >> (16 * (e & 1)));
+          if (n + e < a.N) o[e] = (uint16_t)(x[e / 2] >> (16 * (e & 1)));
       }
     }
   }
@@ -591,12 +653,7 @@ template <int MT, int RS, int CT, int NB>
 void launch_up(const LoraArgs& a, hipStream_t stream) {
   const int64_t rows = MT * kTile, cols = kUpWaves * CT * 16;
   const dim3 grid((unsigned)((a.T + rows - 1) / rows * ((a.N + cols - 1) / cols)), 1, a.up_Q);
-  const bool vec = (((uintptr_t)a.out | (uintptr_t)a.base) & 15) == 0 && a.ld_out % 8 == 0 &&
-                   (!a.base || a.ld_base % 8 == 0);
-  if (vec)
-    hipLaunchKernelGGL((lora_up_kernel<MT, RS, CT, NB, true>), grid, dim3(64 * kUpWaves), 0, stream, a);
-  else
-    hipLaunchKernelGGL((lora_up_kernel<MT, RS, CT, NB, false>), grid, dim3(64 * kUpWaves), 0, stream, a);
+  hipLaunchKernelGGL((lora_up_kernel<MT, RS, CT, NB>), grid, dim3(64 * kUpWaves), 0, stream, a);
 }
 
 }  // namespace
@@ -604,28 +661,32 @@ void launch_up(const LoraArgs& a, hipStream_t stream) {
 void lora_plan(LoraArgs* a) {
   const int64_t T = a->T, K = a->K;
   auto cdiv = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
-  // first kernel
-  const int64_t most = K >= 512 ? K / 512 : 1;             // parts: a piece a wave at least
+  a->h_part = T * a->R;
+  // parts: a wave's first loads (down_products) take a part's pieces at once
+  const int rt = a->R <= 16 ? 1 : a->R <= 32 ? 2 : a->R <= 64 ? 4 : 8;
+  auto most = [&](int mt) { return cdiv(K, 512 * (mt + rt <= 2 ? 4 : mt + rt <= 4 ? 2 : 1)); };
   if (T <= kLoraFewRows) {
     a->mt = 0;
-    const int64_t S = cdiv(256, T);
-    a->S = (int)(S < most ? S : most);
+    a->S = (int)(cdiv(256, T) < most(1) ? cdiv(256, T) : most(1));
   } else {
     const int64_t rows = T < kLoraRows ? T : kLoraRows;
     int mt = a->R <= 64 ? 4 : 2;
-    while (mt > 1 && cdiv(rows, mt * kTile) * most < 256) mt /= 2;
+    while (mt > 1 && cdiv(rows, mt * kTile) * cdiv(K, 512) < 256) mt /= 2;
     const int64_t S = cdiv(256, cdiv(rows, mt * kTile)) + 1;
     a->mt = mt;
-    a->S = (int)(S < most ? S : most < 2 ? 2 : most);
+    a->S = (int)(S < most(mt) ? S : most(mt) < 2 ? 2 : most(mt));
     a->grid = 256;
   }
   // second kernel
-  a->up_mt = T <= 16 ? 1 : 4;
+  // 64 rows share an adapter's weights where they are many (R > 32), else 32: 4096 x 7168 of
+  // rank 16 32.9 us with 64 rows a workgroup, 30.5 with 32; 8192 x 7168 of rank 64 79 and 81
+  a->up_mt = a->R <= 32 ? (T <= 64 ? 1 : 2) : T <= 16 ? 1 : 4;
   const int64_t up_tiles = cdiv(T, a->up_mt * kTile) * cdiv(a->N, a->up_mt == 1 ? 128 : 256);
-  int Q = 1;
-  while (Q < 16 && Q < T && 2 * Q * up_tiles <= 512) Q *= 2;
-  a->up_Q = Q;
-  a->h_part = T * a->R;
+  // workgroups on the same rows: those that find nothing to do cost little beside few others
+  const bool few = T <= kLoraFewRows;
+  a->up_Q = 1;
+  while (a->up_Q < (few ? 16 : 4) && a->up_Q < T && 2 * a->up_Q * up_tiles <= (few ? 512 : 2048))
+    a->up_Q *= 2;
 }
 
 void launch_lora(const LoraArgs& all, hipStream_t stream) {
@@ -642,15 +703,9 @@ void launch_lora(const LoraArgs& all, hipStream_t stream) {
     else if (a.mt == 4) launch_down<4>(a, stream);
     else if (a.mt == 2) launch_down<2>(a, stream);
     else launch_down<1>(a, stream);
-    if (a.up_mt == 1) {
-      if (a.R <= 32) launch_up<1, 1, 2, 4>(a, stream);
-      else if (a.R <= 64) launch_up<1, 2, 2, 2>(a, stream);
-      else launch_up<1, 4, 2, 1>(a, stream);
-    } else {
-      if (a.R <= 32) launch_up<4, 1, 4, 2>(a, stream);
-      else if (a.R <= 64) launch_up<4, 2, 4, 1>(a, stream);
-      else launch_up<4, 4, 4, 1>(a, stream);
-    }
+    if (a.R <= 32) a.up_mt == 1 ? launch_up<1, 1, 2, 4>(a, stream) : launch_up<2, 1, 4, 2>(a, stream);
+    else if (a.R <= 64) a.up_mt == 1 ? launch_up<1, 2, 2, 2>(a, stream) : launch_up<4, 2, 4, 1>(a, stream);
+    else a.up_mt == 1 ? launch_up<1, 4, 2, 1>(a, stream) : launch_up<4, 4, 4, 1>(a, stream);
   }
 }
 

@@ -71,7 +71,8 @@ struct LoraArgs {
   int64_t T, N;
   int K, R, L;
   // the plan for the sizes (lora_plan)
-  int mt;                      // first kernel: row tiles of 16 a workgroup; 0: for few rows
+  int mt;                      // first kernel: row tiles of 16 a workgroup; 0: the one for
+                               // few rows
   int S;                       // parts of the sums over K, at most
   int grid;                    // workgroups of the kernel for many rows
   int up_mt;                   // second kernel: row tiles of 16 a workgroup

@@ -65,7 +65,8 @@ extern "C" {
 
 size_t dg_moe_route_workspace_bytes(int64_t T, int64_t E) {
   if (!route_shape(T, E, 1, E)) return 0;
-  return dg::kRouteWsHeader + (size_t)dg::route_slots(T, E) * (8 * (size_t)E + 4);
+  const size_t slots = (size_t)dg::route_slots(T, E);
+  return slots ? dg::kRouteWsHeader + slots * (8 * (size_t)E + 4) : 0;
 }
 
 dg_status dg_moe_route(const void* logits, int dtype, int64_t ld, const float* bias,
@@ -82,8 +83,8 @@ dg_status dg_moe_route(const void* logits, int dtype, int64_t ld, const float* b
   if (!aligned(logits, bf16 ? 2 : 4) || !aligned(bias, 4) || !aligned(ids, 4) ||
       !aligned(weights, 4) || !aligned(counts, 4) || !aligned(loss, 4) || !aligned(coef, 4))
     return DG_ERR_ALIGN;
-  if (counts && (!workspace || !aligned(workspace, 16) ||
-                 workspace_bytes < dg_moe_route_workspace_bytes(T, E)))
+  const size_t need = counts ? dg_moe_route_workspace_bytes(T, E) : 0;
+  if (need > 0 && (!workspace || !aligned(workspace, 16) || workspace_bytes < need))
     return DG_ERR_WORKSPACE;
   const dg_status st = check_device();
   if (st != DG_OK) return st;

@@ -68,15 +68,18 @@ def _device(t, name):
 
 def _workspace(need, device, workspace, stream, raw):
     """The caller's workspace, or one kept per (device, launch stream) and grown as needed,
-    whatever it holds.  Under graph capture each call gets one from the graph's memory."""
+    whatever it holds: the tensor (kept by the caller until the launch), its pointer and
+    size.  Under graph capture each call gets one from the graph's memory."""
+    if need == 0:
+        return None, None, 0
     if workspace is not None:
         if workspace.device != device or not workspace.is_contiguous():
             raise ValueError(f"workspace must be contiguous and on {device}")
-        return workspace, workspace.numel() * workspace.element_size()
+        return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
     key = (device.index, raw)
     ws = _workspaces.get(key)
     if ws is not None and ws.numel() >= need and not torch.cuda.is_current_stream_capturing():
-        return ws, ws.numel()
+        return ws, ws.data_ptr(), ws.numel()
     st = stream if stream is not None else torch.cuda.current_stream(device)
     with torch.cuda.stream(st):
         ws = torch.empty(max(need, 1 << 16), dtype=torch.uint8, device=device)
@@ -85,7 +88,7 @@ def _workspace(need, device, workspace, stream, raw):
             # memory out again in this stream's order
             with binding._lock:
                 _workspaces[key] = ws
-    return ws, ws.numel()
+    return ws, ws.data_ptr(), ws.numel()
 
 
 def _score(score):
@@ -146,12 +149,12 @@ def dg_moe_route(logits, k, *, bias=None, row_valid=None, score="softmax", norma
     p_coef = _vector(coef, "coef", torch.float32, (E,), dev)
     lib = load_library()
     raw = _raw_stream(dev, stream)
-    ws, ws_bytes = None, 0
+    ws, p_ws, ws_bytes = None, None, 0
     if counts is not None:
-        ws, ws_bytes = _workspace(lib.dg_moe_route_workspace_bytes(T, E), dev, workspace, stream, raw)
+        ws, p_ws, ws_bytes = _workspace(lib.dg_moe_route_workspace_bytes(T, E), dev, workspace, stream, raw)
     st = lib.dg_moe_route(p_logits, _IN_DTYPES[logits.dtype], ld, p_bias, p_valid, T, E, k, sc,
                           bool(normalize), scale, balance or 0.0, p_ids, p_weights, p_counts,
-                          p_loss, p_coef, None if ws is None else ws.data_ptr(), ws_bytes, raw)
+                          p_loss, p_coef, p_ws, ws_bytes, raw)
     if st != 0:
         raise DGError(st, "dg_moe_route")
     return ids, weights, counts, loss, coef
@@ -249,9 +252,10 @@ def dg_lora_bf16(X, A, B, ids, base=None, out=None, *, scales=None, ranks=None, 
     p_out, ld_out = _rows(out, "out", bf16, (T, N), dev)
     lib = load_library()
     raw = _raw_stream(dev, stream)
-    ws, ws_bytes = _workspace(lib.dg_lora_workspace_bytes(T, N, K, R, L), dev, workspace, stream, raw)
+    ws, p_ws, ws_bytes = _workspace(lib.dg_lora_workspace_bytes(T, N, K, R, L), dev, workspace, stream,
+                                    raw)
     st = lib.dg_lora_bf16(p_x, ldx, p_a, p_b, p_ids, p_s, p_r, p_base, ld_base, p_out, ld_out, T, N,
-                          K, R, L, ws.data_ptr(), ws_bytes, raw)
+                          K, R, L, p_ws, ws_bytes, raw)
     if st != 0:
         raise DGError(st, "dg_lora_bf16")
     return out

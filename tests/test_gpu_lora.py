@@ -316,5 +316,6 @@ def test_refusals():
         dg.dg_lora_bf16(x, A, B, ids[:4])
     with pytest.raises(ValueError):
         dg.dg_lora_bf16(x, A.transpose(0, 1).contiguous().transpose(0, 1), B, ids)
-    with pytest.raises(dg.DGError):
-        dg.dg_lora_bf16(x, A, B, ids, workspace=torch.zeros(16, dtype=torch.uint8, device=DEV))
+    with pytest.raises(dg.DGError):                       # a batch that needs a workspace
+        dg.dg_lora_bf16(x.repeat(30, 1), A, B, ids.repeat(30),
+                        workspace=torch.zeros(16, dtype=torch.uint8, device=DEV))

@@ -339,6 +339,7 @@ def test_refusals():
     with pytest.raises(ValueError):
         dg.dg_moe_route(z.cpu(), 2)
     with pytest.raises(dg.DGError):
-        dg.dg_moe_route(z, 2, count=True, workspace=torch.zeros(16, dtype=torch.uint8, device=DEV))
+        dg.dg_moe_route(z.repeat(500, 1), 2, count=True,
+                        workspace=torch.zeros(16, dtype=torch.uint8, device=DEV))
     with pytest.raises(TypeError):
         dg.dg_moe_route_backward(z, torch.zeros(8, 2, device=DEV), coef=torch.zeros(16, device=DEV))

@@ -34,17 +34,18 @@ def test_route_codes(lib):
     assert route(lib, z=None) == 1
     assert route(lib, ids=None) == 1
     assert route(lib, w=None) == 1
-    need = lib.dg_moe_route_workspace_bytes(8, 64)
-    assert need >= 256
+    need = lib.dg_moe_route_workspace_bytes(5000, 64)
+    assert need > 64 * 8
     assert route(lib, counts=A4, loss=A4, ws=A16, wsb=need) == 1          # loss without coef
     assert route(lib, loss=A4, coef=A4, ws=A16, wsb=need) == 1            # loss without counts
     assert route(lib, z=A16 + 2) == 3
     assert route(lib, z=A16 + 1, dtype=1) == 3
     assert route(lib, ids=A4 + 1) == 3
     assert route(lib, bias=A4 + 2) == 3
-    assert route(lib, counts=A4) == 4
-    assert route(lib, counts=A4, ws=A16, wsb=need - 1) == 4
-    assert route(lib, counts=A4, ws=A16 + 8, wsb=need) == 4
+    assert route(lib, T=5000, counts=A4) == 4
+    assert route(lib, T=5000, counts=A4, ws=A16, wsb=need - 1) == 4
+    assert route(lib, T=5000, counts=A4, ws=A16 + 8, wsb=need) == 4
+    assert lib.dg_moe_route_workspace_bytes(1, 64) == 0        # a row alone needs none
     assert lib.dg_moe_route_workspace_bytes(8, 0) == 0
 
 
@@ -68,7 +69,7 @@ def test_backward_codes(lib):
 
 
 def lora(lib, X=A16, ldx=512, A=A16, B=A16, ids=A4, scales=None, ranks=None, base=None, ldb=0, out=A16,
-         ldo=256, T=8, N=256, K=512, R=16, L=4, ws=A16, wsb=1 << 30):
+         ldo=256, T=200, N=256, K=512, R=16, L=4, ws=A16, wsb=1 << 30):
     return lib.dg_lora_bf16(X, ldx, A, B, ids, scales, ranks, base, ldb, out, ldo, T, N, K, R, L, ws, wsb,
                             None)
 
@@ -86,8 +87,8 @@ def test_lora_codes(lib):
         assert lora(lib, **{name: A16 + 8}) == 3, name
     assert lora(lib, ids=A4 + 2) == 3
     assert lora(lib, out=A16 + 1) == 3
-    need = lib.dg_lora_workspace_bytes(8, 256, 512, 16, 4)
-    assert need >= 8 * 16 * 4
+    need = lib.dg_lora_workspace_bytes(200, 256, 512, 16, 4)
+    assert need >= 200 * 16 * 4
     assert lora(lib, wsb=need - 1) == 4
     assert lora(lib, ws=None) == 4
     assert lora(lib, ws=A16 + 8) == 4
