@@ -319,7 +319,7 @@ route_kernel(RouteArgs a) {
 
     // lane l of the row keeps the choices l, l + L, ...
     int ids[KP];
-    float w[KP], total = 0.0f;
+    float w[KP];
 #pragma unroll
     for (int q = 0; q < KP; ++q) {
       const int j = q * L + l;
@@ -333,12 +333,18 @@ route_kernel(RouteArgs a) {
         w[q] = a.sigmoid ? sigmoid(zc) : exp_of(zc - n.max) * n.inv;
         if (sums) atomicAdd(&hist[ids[q]], 1);
       }
-      total += w[q];
     }
     float f = a.scale;
     if (a.normalize) {
-      total = group_sum<L>(total);
-      f = total == 0.0f ? 0.0f : a.scale / total;
+      // in pairs, pairs of pairs ... of the choices, whatever L is
+      float part[KP];
+#pragma unroll
+      for (int q = 0; q < KP; ++q) part[q] = group_sum<L>(w[q]);
+#pragma unroll
+      for (int d = 1; d < KP; d *= 2)
+#pragma unroll
+        for (int q = 0; q < KP; q += 2 * d) part[q] += part[q + d];
+      f = part[0] == 0.0f ? 0.0f : a.scale / part[0];
     }
 #pragma unroll
     for (int q = 0; q < KP; ++q) {
@@ -635,29 +641,42 @@ int lanes_for(int64_t E, int V) {
 
 // Forward launch shape.  Few experts a lane (V = 8) spread a row over more lanes: shorter
 // chains, for calls that do not fill the GPU.  Many (V = 32) leave less to merge across
-// lanes: less work in all.
+// lanes: less work in all.  With `counts` under sigmoid, rows that one workgroup takes in two
+// passes are left to one, which needs no second kernel (64 x 256 with counts, one call after the
+// other: 12.1 us as two kernels on 16 workgroups, 8.6 as one).  Under softmax the sum over a
+// row, and with it the weights' last bits, would then differ from those of a call that asks
+// for no counts.
 struct Shape {
   int V, L, grid;
 };
-Shape forward_shape(int64_t T, int64_t E) {
+Shape forward_shape(int64_t T, int64_t E, bool one_if_small) {
   Shape h;
-  h.V = E > 512 || T * E >= kRouteWideWork ? 32 : 8;
-  h.L = lanes_for(E, h.V);
-  if (h.V == 32 && h.L < 2) h.L = 2;
-  const int64_t rows = (int64_t)kWaves * 64 / h.L, blocks = (T + rows - 1) / rows;
-  h.grid = (int)(blocks < 1 ? 1 : blocks < kRouteMaxGrid ? blocks : kRouteMaxGrid);
+  auto set = [&](int V) {
+    h.V = V;
+    h.L = lanes_for(E, V);
+    if (V == 32 && h.L < 2) h.L = 2;
+    const int64_t rows = (int64_t)kWaves * 64 / h.L, blocks = (T + rows - 1) / rows;
+    h.grid = (int)(blocks < 1 ? 1 : blocks < kRouteMaxGrid ? blocks : kRouteMaxGrid);
+  };
+  set(E > 512 || T * E >= kRouteWideWork ? 32 : 8);
+  if (one_if_small && h.grid > 1) {
+    const Shape few = h;
+    set(E > 16 ? 32 : 8);
+    if (h.grid > 2) return few;
+    h.grid = 1;
+  }
   return h;
 }
 
 }  // namespace
 
 int route_slots(int64_t T, int64_t E) {
-  const int g = forward_shape(T, E).grid;
+  const int g = forward_shape(T, E, false).grid;
   return g > 1 ? g : 0;
 }
 
 void launch_route(const RouteArgs& a, hipStream_t stream) {
-  const Shape h = forward_shape(a.T, a.E);
+  const Shape h = forward_shape(a.T, a.E, a.sigmoid && a.counts);
   if (h.V == 32) {
     switch (h.L) {
       case 2: return launch_forward<2, 32>(a, h.grid, stream);

@@ -23,35 +23,29 @@ def dg_lora_workspace_bytes(T: int, N: int, K: int, R: int, L: int) -> int:
 
 
 # ------------------------------------------------------------------------ marshalling
+# A decode step makes these calls once a layer with little for the GPU to do, so the usual
+# case of every check is one expression and what is wrong is found out afterwards.
 def _vector(t, name, dtype, shape, device):
     """Pointer of an optional dense argument (None: a null pointer)."""
     if t is None:
         return None
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t.data_ptr()
+    binding._check(t, name, dtype, shape, device)
     return t.data_ptr()
 
 
 def _rows(t, name, dtype, shape, device):
     """Pointer and row stride of a matrix whose rows are dense but may lie apart."""
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    ld, one = t.stride()
-    if one != 1 and shape[1] > 1 and shape[0] > 0:
+    if t.dtype is dtype and t.shape == shape and t.device == device:
+        ld, one = t.stride()
+        if shape[0] <= 1:                    # no or one row: the stride says nothing
+            return t.data_ptr(), shape[1]
+        if one == 1 or shape[1] <= 1:
+            return t.data_ptr(), ld
         raise ValueError(f"{name} must have dense rows, got strides {(ld, one)}")
-    if shape[0] <= 1:                    # no or one row: the stride says nothing
-        ld = shape[1]
-    return t.data_ptr(), ld
+    binding._check(t, name, dtype, shape, device)
+    raise ValueError(f"{name}: not a matrix this call takes")
 
 
 def _raw_stream(device, stream):
@@ -61,7 +55,7 @@ def _raw_stream(device, stream):
 
 
 def _device(t, name):
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be on a GPU, got {t.device}")
     return t.device
 
@@ -77,24 +71,29 @@ def _workspace(need, device, workspace, stream, raw):
             raise ValueError(f"workspace must be contiguous and on {device}")
         return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
     key = (device.index, raw)
-    ws = _workspaces.get(key)
-    if ws is not None and ws.numel() >= need and not torch.cuda.is_current_stream_capturing():
-        return ws, ws.data_ptr(), ws.numel()
+    kept = _workspaces.get(key)
+    enough = kept is not None and kept[2] >= need
+    if enough and stream is None and not torch.cuda.is_current_stream_capturing():
+        return kept
     st = stream if stream is not None else torch.cuda.current_stream(device)
     with torch.cuda.stream(st):
+        capturing = torch.cuda.is_current_stream_capturing()
+        if enough and not capturing:
+            return kept
         ws = torch.empty(max(need, 1 << 16), dtype=torch.uint8, device=device)
-        if not torch.cuda.is_current_stream_capturing():
+        if not capturing:
             # a smaller one was used on this stream only, so the allocator may hand its
             # memory out again in this stream's order
             with binding._lock:
-                _workspaces[key] = ws
+                _workspaces[key] = (ws, ws.data_ptr(), ws.numel())
     return ws, ws.data_ptr(), ws.numel()
 
 
 def _score(score):
-    if score not in _SCORES:
+    code = _SCORES.get(score)
+    if code is None:
         raise ValueError(f"unknown score function {score!r} (softmax or sigmoid)")
-    return _SCORES[score]
+    return code
 
 
 def _logits(logits):
@@ -147,7 +146,7 @@ def dg_moe_route(logits, k, *, bias=None, row_valid=None, score="softmax", norma
     p_counts = _vector(counts, "counts", torch.int32, (E,), dev)
     p_loss = _vector(loss, "loss", torch.float32, (), dev)
     p_coef = _vector(coef, "coef", torch.float32, (E,), dev)
-    lib = load_library()
+    lib = binding._lib or load_library()
     raw = _raw_stream(dev, stream)
     ws, p_ws, ws_bytes = None, None, 0
     if counts is not None:
@@ -184,7 +183,7 @@ def dg_moe_route_backward(logits, ids, *, grad_weights=None, coef=None, grad_los
     if grad_logits is None:
         grad_logits = torch.empty((T, E), dtype=logits.dtype, device=dev)
     p_out, ld_out = _rows(grad_logits, "grad_logits", logits.dtype, (T, E), dev)
-    st = load_library().dg_moe_route_backward(
+    st = (binding._lib or load_library()).dg_moe_route_backward(
         p_logits, _IN_DTYPES[logits.dtype], ld, p_valid, T, E, k, sc, bool(normalize), scale, p_ids,
         p_gw, p_coef, p_gl, p_out, ld_out, _raw_stream(dev, stream))
     if st != 0:
@@ -250,7 +249,7 @@ def dg_lora_bf16(X, A, B, ids, base=None, out=None, *, scales=None, ranks=None, 
     if out is None:
         out = torch.empty((T, N), dtype=bf16, device=dev)
     p_out, ld_out = _rows(out, "out", bf16, (T, N), dev)
-    lib = load_library()
+    lib = binding._lib or load_library()
     raw = _raw_stream(dev, stream)
     ws, p_ws, ws_bytes = _workspace(lib.dg_lora_workspace_bytes(T, N, K, R, L), dev, workspace, stream,
                                     raw)
