@@ -81,6 +81,14 @@ __device__ __forceinline__ float group_sum(float v) {
   else return v;
 }
 
+// What the wave's lanes have written to LDS is there for the others, and stays as it is until
+// all have read it (a wave's LDS accesses are carried out in order).
+__device__ __forceinline__ void wave_lds_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // --------------------------------------------------------------------- choosing experts
 __device__ __forceinline__ double pack_key(float key, int e) {
   const int bits = __float_as_int(fmaxf(key, -INFINITY));      // NaN: -inf
@@ -154,10 +162,10 @@ __device__ __forceinline__ void merge_lanes(double (&list)[N]) {
 __device__ __forceinline__ float load_one(const void* p, int64_t i, int bf16) {
   return bf16 ? __uint_as_float((uint32_t)((const uint16_t*)p)[i] << 16) : ((const float*)p)[i];
 }
-__device__ __forceinline__ uint16_t to_bf16(float f) {
-  const uint32_t u = __float_as_uint(f);
-  if ((u & 0x7FFFFFFFu) > 0x7F800000u) return 0x7FC0;
-  return (uint16_t)((u + 0x7FFFu + ((u >> 16) & 1u)) >> 16);
+// Two numbers rounded to bf16 (to nearest even), the first in the low half.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  using bf16x2 = __attribute__((ext_vector_type(2))) __bf16;
+  return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)lo, (__bf16)hi});
 }
 
 // A row's V logits of this lane; `fill` past the last expert.
@@ -478,46 +486,70 @@ static_assert((kRouteMaxE + kSumMinCols - 1) / kSumMinCols <= 64, "one lane a pa
 static_assert(4 * (1 + 64) <= kRouteWsHeader, "header");
 
 // ----------------------------------------------------------------------------- backward
-// dz from the weights' gradients (scattered to the chosen experts through a row of LDS)
-// and the loss's (coef, the same for every row).
+// dz from the weights' gradients and the loss's (coef, the same for every row).  A row's
+// scores go through a row of LDS, where the lanes that keep its choices pick theirs up, and
+// the choices' score gradients through another, which is zero but for them.  A wave's next
+// rows are loaded before its present ones are worked on.
 template <int L, int V>
 __global__ void __launch_bounds__(kThreads)
 route_backward_kernel(RouteArgs a) {
   constexpr int RW = 64 / L, EP = L * V;
-  constexpr int KP = L >= kRouteMaxK ? 1 : kRouteMaxK / L;
-  __shared__ float rows_d[kWaves * RW][EP];
+  constexpr int KP = L >= kRouteMaxK ? 1 : kRouteMaxK / L;   // choices of a lane
+  __shared__ __attribute__((aligned(16))) float rows_s[kWaves * RW][EP], rows_d[kWaves * RW][EP];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int l = lane % L, sub = lane / L;
-  float* d = rows_d[wave * RW + sub];
-#pragma unroll
-  for (int v = 0; v < V; ++v) d[4 * ((v / 4) * L + l) + (v & 3)] = 0.0f;
-
+  float* sr = rows_s[wave * RW + sub];
+  float* dr = rows_d[wave * RW + sub];
   float u[V];
   const float g_loss = a.coef ? (a.grad_loss ? *a.grad_loss : 1.0f) : 0.0f;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int e = 4 * ((v / 4) * L + l) + (v & 3);
+    dr[e] = 0.0f;
     u[v] = a.coef && e < a.E ? g_loss * a.coef[e] : 0.0f;
   }
   const int64_t step = (int64_t)gridDim.x * kWaves * RW;
-  for (int64_t row0 = ((int64_t)blockIdx.x * kWaves + wave) * RW; row0 < a.T; row0 += step) {
-    const int64_t row = row0 + sub;
-    const bool in = row < a.T;
-    const bool live = in && (!a.row_valid || a.row_valid[row] != 0);
-    float z[V], s[V], c[V];
-    if (live) {
-      load_row<L, V>(a, row, l, -INFINITY, z);
-    } else {
+  const int64_t first = ((int64_t)blockIdx.x * kWaves + wave) * RW;
+
+  float z[V], gw[KP];
+  int id[KP], valid;
+  auto load = [&](int64_t row) {
+    const int64_t at = row < a.T ? row : a.T - 1;
+    load_row<L, V>(a, at, l, -INFINITY, z);
+    valid = row < a.T && (!a.row_valid || a.row_valid[at] != 0);
 #pragma unroll
-      for (int v = 0; v < V; ++v) z[v] = -INFINITY;
+    for (int q = 0; q < KP; ++q) {
+      const int j = q * L + l;
+      id[q] = -1;
+      gw[q] = 0.0f;
+      if (a.grad_weights && j < a.k) {
+        id[q] = a.ids_in[at * a.k + j];
+        gw[q] = a.grad_weights[at * a.k + j];
+      }
     }
+  };
+  if (first < a.T) load(first + sub);
+  for (int64_t row0 = first; row0 < a.T; row0 += step) {
+    const int64_t row = row0 + sub;
+    float x[V], s[V], c[V], g[KP];
+    int chosen[KP];
+    const bool live = valid;
+#pragma unroll
+    for (int v = 0; v < V; ++v) x[v] = z[v];      // of padding whatever it holds: not used
+#pragma unroll
+    for (int q = 0; q < KP; ++q) {
+      chosen[q] = live && id[q] >= 0 && id[q] < a.E ? id[q] : -1;
+      g[q] = chosen[q] >= 0 ? a.scale * gw[q] : 0.0f;
+    }
+    if (row0 + step < a.T) load(row + step);
+
     RowNorm n{0.0f, 0.0f};
     float us = 0.0f;                              // sum of u p over the row
     if (a.sigmoid) {
       float sum = 0.0f;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        s[v] = sigmoid(z[v], &c[v]);
+        s[v] = sigmoid(x[v], &c[v]);
         sum += s[v];
         us = __builtin_fmaf(u[v], s[v], us);
       }
@@ -525,7 +557,7 @@ route_backward_kernel(RouteArgs a) {
       n.inv = sum == 0.0f ? 0.0f : 1.0f / sum;
       us = group_sum<L>(us) * n.inv;
     } else {
-      n = softmax_row<L, V>(z, s);
+      n = softmax_row<L, V>(x, s);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         s[v] *= n.inv;
@@ -533,81 +565,76 @@ route_backward_kernel(RouteArgs a) {
       }
       us = group_sum<L>(us);
     }
-    // the chosen experts' score gradients
-    int id[KP];
-    float gw[KP], sc[KP], total = 0.0f, dot = 0.0f;
+    float ds = 0.0f;                              // sum of D s over the chosen: 0 if normalized
+    if (a.grad_weights) {
 #pragma unroll
-    for (int q = 0; q < KP; ++q) {
-      const int j = q * L + l;
-      id[q] = -1;
-      gw[q] = sc[q] = 0.0f;
-      if (live && a.grad_weights && j < a.k) {
-        const int e = a.ids_in[row * a.k + j];
-        if (e >= 0 && e < a.E) {
-          id[q] = e;
-          gw[q] = a.scale * a.grad_weights[row * a.k + j];
-          const float zc = load_one(a.logits, row * a.ld + e, a.bf16);
-          sc[q] = a.sigmoid ? sigmoid(zc) : exp_of(zc - n.max) * n.inv;
+      for (int q = 0; q < V / 4; ++q)
+        *(float4*)&sr[4 * (q * L + l)] = make_float4(s[4 * q], s[4 * q + 1], s[4 * q + 2], s[4 * q + 3]);
+      wave_lds_sync();
+      float sc[KP], total = 0.0f, dot = 0.0f;
+#pragma unroll
+      for (int q = 0; q < KP; ++q) {
+        sc[q] = chosen[q] >= 0 ? sr[chosen[q]] : 0.0f;
+        total += sc[q];
+        dot = __builtin_fmaf(g[q], sc[q], dot);
+      }
+      if (a.normalize) {
+        total = group_sum<L>(total);
+        dot = group_sum<L>(dot);
+        const float it = total == 0.0f ? 0.0f : 1.0f / total;
+        const float mean = dot * it;
+#pragma unroll
+        for (int q = 0; q < KP; ++q) g[q] = (g[q] - mean) * it;
+      }
+#pragma unroll
+      for (int q = 0; q < KP; ++q)
+        if (chosen[q] >= 0) {
+          dr[chosen[q]] = g[q];
+          ds = __builtin_fmaf(g[q], sc[q], ds);
         }
-      }
-      total += sc[q];
-      dot = __builtin_fmaf(gw[q], sc[q], dot);
+      ds = a.sigmoid || a.normalize ? 0.0f : group_sum<L>(ds);
+      wave_lds_sync();
     }
-    if (a.normalize) {
-      total = group_sum<L>(total);
-      dot = group_sum<L>(dot);
-      const float it = total == 0.0f ? 0.0f : 1.0f / total;
-      const float mean = dot * it;
-#pragma unroll
-      for (int q = 0; q < KP; ++q) gw[q] = (gw[q] - mean) * it;
-    }
-    float ds = 0.0f;                              // sum of D s over the chosen
-#pragma unroll
-    for (int q = 0; q < KP; ++q)
-      if (id[q] >= 0) {
-        d[id[q]] = gw[q];
-        ds = __builtin_fmaf(gw[q], sc[q], ds);
-      }
-    ds = group_sum<L>(ds);
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
     float dz[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float dv = d[4 * ((v / 4) * L + l) + (v & 3)];
-      dz[v] = a.sigmoid ? ((u[v] - us) * n.inv + dv) * c[v] : s[v] * (u[v] + dv - (us + ds));
-    }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-#pragma unroll
-    for (int q = 0; q < KP; ++q)
-      if (id[q] >= 0) d[id[q]] = 0.0f;
-    if (!in) continue;
-    const int64_t at = row * a.ld_grad;
-#pragma unroll
     for (int q = 0; q < V / 4; ++q) {
-      const int e = 4 * (q * L + l);
-      if (!live)
-        for (int i = 0; i < 4; ++i) dz[4 * q + i] = 0.0f;
-      if (a.vec_grad) {
-        if (e < a.E) {
-          if (a.bf16)
-            *(uint2*)((uint16_t*)a.grad_logits + at + e) =
-                make_uint2(to_bf16(dz[4 * q]) | ((uint32_t)to_bf16(dz[4 * q + 1]) << 16),
-                           to_bf16(dz[4 * q + 2]) | ((uint32_t)to_bf16(dz[4 * q + 3]) << 16));
-          else
-            *(float4*)((float*)a.grad_logits + at + e) =
-                make_float4(dz[4 * q], dz[4 * q + 1], dz[4 * q + 2], dz[4 * q + 3]);
-        }
-      } else {
+      const float4 d = a.grad_weights ? *(const float4*)&dr[4 * (q * L + l)] : make_float4(0, 0, 0, 0);
+      const float dv[4] = {d.x, d.y, d.z, d.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (e + i < a.E) {
-            if (a.bf16) ((uint16_t*)a.grad_logits)[at + e + i] = to_bf16(dz[4 * q + i]);
-            else ((float*)a.grad_logits)[at + e + i] = dz[4 * q + i];
+      for (int i = 0; i < 4; ++i) {
+        const int v = 4 * q + i;
+        const float r = a.sigmoid ? ((u[v] - us) * n.inv + dv[i]) * c[v] : s[v] * (u[v] + dv[i] - (us + ds));
+        dz[v] = live ? r : 0.0f;
+      }
+    }
+    if (a.grad_weights) {
+      wave_lds_sync();
+#pragma unroll
+      for (int q = 0; q < KP; ++q)
+        if (chosen[q] >= 0) dr[chosen[q]] = 0.0f;
+    }
+    if (row < a.T) {
+      const int64_t at = row * a.ld_grad;
+#pragma unroll
+      for (int q = 0; q < V / 4; ++q) {
+        const int e = 4 * (q * L + l);
+        if (a.vec_grad) {
+          if (e < a.E) {
+            if (a.bf16)
+              *(uint2*)((uint16_t*)a.grad_logits + at + e) =
+                  make_uint2(pack_bf16(dz[4 * q], dz[4 * q + 1]), pack_bf16(dz[4 * q + 2], dz[4 * q + 3]));
+            else
+              *(float4*)((float*)a.grad_logits + at + e) =
+                  make_float4(dz[4 * q], dz[4 * q + 1], dz[4 * q + 2], dz[4 * q + 3]);
           }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (e + i < a.E) {
+              if (a.bf16) ((uint16_t*)a.grad_logits)[at + e + i] = (uint16_t)pack_bf16(dz[4 * q + i], 0.0f);
+              else ((float*)a.grad_logits)[at + e + i] = dz[4 * q + i];
+            }
+        }
       }
     }
   }
@@ -698,16 +725,33 @@ void launch_route(const RouteArgs& a, hipStream_t stream) {
 }
 
 void launch_route_backward(const RouteArgs& a, hipStream_t stream) {
-  int L = lanes_for(a.E, 16);
-  if (L < 4) L = 4;
+  // few experts a lane while the call does not fill the GPU (4099 x 60: 3.3 us with 4, 4.1 with
+  // 8), more, and fewer steps across lanes, once it does (32768 x 256: 16.4 us with 8, 17.8
+  // with 4, 20.7 with 16, whose registers leave too few waves)
+  const int V = a.E > 512 ? 16 : a.E > 256 || a.T * a.E >= kRouteWideWork / 2 ? 8 : 4;
+  const int L = lanes_for(a.E, V);
   const int64_t rows = (int64_t)kWaves * 64 / L, blocks = (a.T + rows - 1) / rows;
-  const int grid = (int)(blocks < 512 ? blocks : 512);
+  const int grid = (int)(blocks < 1024 ? blocks : 1024);
+  if (V == 16) return launch_backward<64, 16>(a, grid, stream);
+  if (V == 8) {
+    switch (L) {
+      case 1: return launch_backward<1, 8>(a, grid, stream);
+      case 2: return launch_backward<2, 8>(a, grid, stream);
+      case 4: return launch_backward<4, 8>(a, grid, stream);
+      case 8: return launch_backward<8, 8>(a, grid, stream);
+      case 16: return launch_backward<16, 8>(a, grid, stream);
+      case 32: return launch_backward<32, 8>(a, grid, stream);
+      default: return launch_backward<64, 8>(a, grid, stream);
+    }
+  }
   switch (L) {
-    case 4: return launch_backward<4, 16>(a, grid, stream);
-    case 8: return launch_backward<8, 16>(a, grid, stream);
-    case 16: return launch_backward<16, 16>(a, grid, stream);
-    case 32: return launch_backward<32, 16>(a, grid, stream);
-    default: return launch_backward<64, 16>(a, grid, stream);
+    case 1: return launch_backward<1, 4>(a, grid, stream);
+    case 2: return launch_backward<2, 4>(a, grid, stream);
+    case 4: return launch_backward<4, 4>(a, grid, stream);
+    case 8: return launch_backward<8, 4>(a, grid, stream);
+    case 16: return launch_backward<16, 4>(a, grid, stream);
+    case 32: return launch_backward<32, 4>(a, grid, stream);
+    default: return launch_backward<64, 4>(a, grid, stream);
   }
 }
 
