@@ -9,7 +9,7 @@
 namespace dg {
 
 // First bytes of the gate's workspace, before its workgroups' sums.
-constexpr int kRouteWsHeader = 512;
+constexpr int kRouteWsHeader = 16;
 
 // The gate and its backward pass (defined in dg_route.hip).
 constexpr int kRouteMaxK = 16;       // choices a row

@@ -225,17 +225,15 @@ __device__ __forceinline__ RowNorm softmax_row(const float (&z)[V], float (&s)[V
 
 // ------------------------------------------------------------------------------ forward
 // What the workgroups of a call with several have counted, in the workspace: [workgroup][E]
-// probabilities, [workgroup][E] choices, [workgroup] live rows; before them the second
-// kernel's arrival counter and its workgroups' parts of the loss.
+// probabilities, [workgroup][E] choices, [workgroup] live rows; before them the word in
+// which the second kernel's workgroups add up the loss.
 struct Parts {
-  int* arrivals;
-  float* loss;
+  unsigned long long* word;
   float* p;
   int* n;
   int* rows;
   __device__ Parts(const RouteArgs& a, int G)
-      : arrivals((int*)a.workspace),
-        loss((float*)a.workspace + 1),
+      : word((unsigned long long*)a.workspace),
         p((float*)((uint8_t*)a.workspace + kRouteWsHeader)),
         n((int*)(p + (int64_t)G * a.E)),
         rows(n + (int64_t)G * a.E) {}
@@ -396,7 +394,7 @@ route_kernel(RouteArgs a) {
   }
   if (G > 1) {
     if (tid == 0) part.rows[b] = live_rows;
-    if (tid == 0 && b == 0) *part.arrivals = 0;
+    if (tid == 0 && b == 0) *part.word = 0;
   } else if (a.loss) {
     sum = group_sum<64>(sum);
     __syncthreads();
@@ -407,72 +405,84 @@ route_kernel(RouteArgs a) {
 }
 
 // Sums over the first kernel's G workgroups: a workgroup takes `cols` experts, its threads
-// one of them and a slice of the G each, then the slices in order.  Of the loss's parts the
-// last workgroup to arrive takes the sum, in workgroup order.
-constexpr int kSumThreads = 1024, kSumMinCols = 16;
+// one of them and a slice of the G each; then the slices of a wave, then the waves, in a
+// fixed order.  The workgroups' parts of the loss meet in one word: the loss is balance * E
+// times sum_e (n_e / (k V)) (p_e / V), a number in [0, 1], which each adds as a multiple of
+// 2^-44 together with one arrival, in one atomic addition; integers add up to the same in
+// any order, and who finds all others arrived has the sum.  (To store parts, arrive and read
+// them back takes three trips to memory instead of one.)
+constexpr int kSumThreads = 1024, kSumMinCols = 16, kSumWaves = kSumThreads / 64;
 
 __global__ void __launch_bounds__(kSumThreads)
 route_sums_kernel(RouteArgs a, int G, int cols) {
-  __shared__ int n_s[kSumThreads], live_s[kSumThreads / 64];
-  __shared__ float p_s[kSumThreads];
-  __shared__ int last;
+  __shared__ int n_s[kSumThreads], live_s[kSumWaves];
+  __shared__ float p_s[kSumThreads], loss_s[kSumWaves];
   const int tid = threadIdx.x, c = tid & (cols - 1), slices = kSumThreads / cols, slice = tid / cols;
   const int e = blockIdx.x * cols + c, ee = e < a.E ? e : a.E - 1;
   Parts part(a, G);
-  int n = 0, live = 0;
+  int n = 0, live = tid < G ? part.rows[tid] : 0;
   float p = 0.0f;
-#pragma unroll 8
-  for (int g = slice; g < G; g += slices) n += part.n[(int64_t)g * a.E + ee];
-  if (a.loss) {
-#pragma unroll 8
-    for (int g = slice; g < G; g += slices) p += part.p[(int64_t)g * a.E + ee];
+  constexpr int U = 8;                     // sums in flight (without a loss p is not used)
+  for (int g0 = slice; g0 < G; g0 += U * slices) {
+    int nv[U];
+    float pv[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int g = g0 + u * slices < G ? g0 + u * slices : slice;
+      nv[u] = part.n[(int64_t)g * a.E + ee];
+      pv[u] = part.p[(int64_t)g * a.E + ee];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (g0 + u * slices < G) {
+        n += nv[u];
+        p += pv[u];
+      }
   }
-  if (tid < G) live = part.rows[tid];
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) live += __shfl_xor(live, off, 64);
+  for (int off = cols; off < 64; off *= 2) {
+    n += __shfl_xor(n, off, 64);
+    p += __shfl_xor(p, off, 64);
+  }
   n_s[tid] = n;
   p_s[tid] = p;
   if ((tid & 63) == 0) live_s[tid >> 6] = live;
   __syncthreads();
   live = 0;
-  for (int w = 0; w < kSumThreads / 64; ++w) live += live_s[w];
+#pragma unroll
+  for (int w = 0; w < kSumWaves; ++w) live += live_s[w];
   float sum = 0.0f;
   if (tid < cols && e < a.E) {
-    for (int w = 1; w < slices; ++w) {
-      n += n_s[w * cols + tid];
-      p += p_s[w * cols + tid];
+    const int each = cols < 64 ? 64 : cols;       // threads between two sums of an expert
+    for (int w = each; w < kSumThreads; w += each) {
+      n += n_s[w + tid];
+      p += p_s[w + tid];
     }
     a.counts[e] = n;
     if (a.loss) {
-      const float cf = coef_of(a, n, live);
-      a.coef[e] = cf;
-      sum = live ? cf * p : 0.0f;
+      a.coef[e] = coef_of(a, n, live);
+      const float rows = (float)live;
+      sum = live ? ((float)n / ((float)a.k * rows)) * (p / rows) : 0.0f;
     }
   }
   if (!a.loss) return;
   sum = group_sum<64>(sum);
-  __syncthreads();
-  if ((tid & 63) == 0) p_s[tid >> 6] = sum;
+  if ((tid & 63) == 0) loss_s[tid >> 6] = sum;
   __syncthreads();
   if (tid >= 64) return;
-  sum = group_sum<16>(p_s[tid & 15]);
-  const int B = (int)gridDim.x;
-  if (B > 1) {
-    // handed over with device-coherent accesses: stores complete before the arrival
-    if (tid == 0) {
-      __hip_atomic_store(part.loss + blockIdx.x, sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      last = __hip_atomic_fetch_add(part.arrivals, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
-             B - 1;
-    }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-    if (!last) return;
-    sum = tid < B ? __hip_atomic_load(part.loss + tid, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0.0f;
-    sum = group_sum<64>(sum);
-  }
-  if (tid == 0) *a.loss = sum;
+  sum = group_sum<16>(loss_s[tid & 15]);
+  if (tid != 0) return;
+  constexpr int kFraction = 44, kCount = 56;
+  constexpr unsigned long long kNaN = 1ull << 48;         // past any sum, 64 of them below kCount
+  const unsigned long long mine =
+      (1ull << kCount) | (sum != sum ? kNaN : (unsigned long long)((double)sum * (1ull << kFraction) + 0.5));
+  const unsigned long long all =
+      mine + __hip_atomic_fetch_add(part.word, mine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if ((int)(all >> kCount) != (int)gridDim.x) return;
+  const unsigned long long x = all & ((1ull << kCount) - 1);
+  const float share = x >= kNaN ? __builtin_nanf("") : (float)((double)x / (1ull << kFraction));
+  *a.loss = a.balance * (float)a.E * share;
 }
 
 // Experts of a workgroup of the second kernel: at most about 16 of the G sums a thread.
@@ -482,8 +492,7 @@ int sum_cols(int E, int G) {
   return cols;
 }
 static_assert(kRouteMaxGrid <= kSumThreads, "one thread a workgroup's live rows");
-static_assert((kRouteMaxE + kSumMinCols - 1) / kSumMinCols <= 64, "one lane a part of the loss");
-static_assert(4 * (1 + 64) <= kRouteWsHeader, "header");
+static_assert((kRouteMaxE + kSumMinCols - 1) / kSumMinCols <= 64, "arrivals");
 
 // ----------------------------------------------------------------------------- backward
 // dz from the weights' gradients and the loss's (coef, the same for every row).  A row's
