@@ -258,12 +258,14 @@ dg_status dg_transpose_fp8(const uint8_t *X, uint8_t *Y, int64_t rows, int64_t c
  * 8 for bf16, with E and ld multiples of 4, are read in wider loads).
  *
  * With counts the call needs a workspace of dg_moe_route_workspace_bytes bytes (0 for a few
- * rows: none), 16-byte aligned.  It may hold anything before and after the call, so one buffer can serve this
- * call and dg_lora_bf16 in stream order (not two calls that may overlap, and not the GEMM
- * calls, which need theirs zero).
+ * rows: none), 16-byte aligned.  It may hold anything before and after the call, so one
+ * buffer can serve this call and dg_lora_bf16 in stream order (not two calls that may
+ * overlap, and not the GEMM calls, which need theirs zero).
  *
  * Sums over rows are taken in an order that depends on the sizes only: the same inputs give
- * the same bits.
+ * the same bits.  Over several workgroups the loss is added up in multiples of
+ * balance * E * 2^-44, at most 64 of them: beside fp32's relative error it has an absolute
+ * one of balance * E * 2^-39 at most.
  * Errors, in this order: DG_ERR_SHAPE, DG_ERR_FORMAT (dtype or score), DG_ERR_NULL,
  * DG_ERR_ALIGN, DG_ERR_WORKSPACE, DG_ERR_DEVICE, DG_ERR_HIP.  Asynchronous on `stream`,
  * no readback, graph-capturable. */
@@ -306,7 +308,8 @@ dg_status dg_moe_route_backward(const void *logits, int dtype, int64_t ld,
  *   base bf16, T x N, row stride ld_base (NULL: zero; may be `out` itself with the same
  *   stride, not overlap it otherwise)         out bf16, T x N, row stride ld_out
  * Rows of one adapter may be anywhere.  A row's result depends on its own adapter's values
- * only, whatever other adapters hold.  Sums are fp32; the inner product is kept to 16
+ * only, whatever other adapters hold; an infinity or NaN in it makes the results that it
+ * takes part in infinite or NaN.  Sums are fp32; the inner product is kept to 16
  * significant bits or more and the result rounded once, to nearest even.
  *
  * T, N >= 0 (0: nothing to do), K > 0 and K % 128 == 0, N, K <= 2^22, 8 <= R <= 128 and

@@ -260,7 +260,8 @@ route_kernel(RouteArgs a) {
   const bool sums = a.counts != nullptr;
   for (int e = tid; e < EP; e += kThreads) {
     hist[e] = 0;
-    bias[e] = a.bias && e < a.E ? a.bias[e] : 0.0f;
+    // a bias of -0 as +0: a key is then never -0, which would lie below the +0 it equals
+    bias[e] = a.bias && e < a.E ? a.bias[e] + 0.0f : 0.0f;
   }
   if (tid == 0) live_rows = 0;
   __syncthreads();

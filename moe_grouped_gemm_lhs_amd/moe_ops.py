@@ -5,6 +5,7 @@ function.  As in binding.py: argument checks and marshalling, no arithmetic, no 
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import binding
 from .binding import _IN_DTYPES, DGError, load_library
@@ -204,6 +205,7 @@ class _Route(torch.autograd.Function):
         return ids, weights, counts, loss
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, _ids, grad_weights, _counts, grad_loss):
         logits, ids, coef, row_valid = ctx.saved_tensors
         if grad_weights is None and grad_loss is None:
@@ -218,7 +220,7 @@ class _Route(torch.autograd.Function):
 def moe_route(logits, k, *, bias=None, row_valid=None, score="softmax", normalize=False, scale=1.0,
               balance=None):
     """dg_moe_route for training: (ids, weights, counts, loss), weights and loss
-    differentiable by logits (loss None without a balance)."""
+    differentiable by logits once (loss None without a balance)."""
     return _Route.apply(logits, k, bias, row_valid, score, normalize, scale, balance)
 
 

@@ -115,6 +115,20 @@ def test_ties_take_the_lowest_index():
     assert np.array_equal(ids, want)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_keys_of_either_zero_are_equal(dtype):
+    """-0 comes out of an addition only where both the logit and the bias are -0."""
+    host = np.zeros((3, 40), np.float32)
+    host[0] = -0.0
+    host[1, ::2] = -0.0
+    bias = np.zeros(40, np.float32)
+    bias[:20] = -0.0
+    bias[30:] = -1.0
+    z = torch.from_numpy(host).to(DEV).to(dtype)
+    ids = dg.dg_moe_route(z, 8, bias=torch.from_numpy(bias).to(DEV))[0].cpu().numpy()
+    assert np.array_equal(ids, np.tile(np.arange(8), (3, 1)))
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_closed_experts_and_empty_rows(score):
     T, E, k = 50, 20, 6
@@ -316,6 +330,10 @@ def test_autograd():
     z.grad = None
     dg.moe_route(z, 4, balance=0.5)[3].backward()
     assert torch.isfinite(z.grad).all() and z.grad.abs().sum() > 0
+    # a second derivative is refused, not left out
+    g, = torch.autograd.grad(dg.moe_route(z, 4, balance=0.5)[3], z, create_graph=True)
+    with pytest.raises(RuntimeError):
+        g.sum().backward()
 
 
 def test_refusals():
