@@ -259,21 +259,59 @@ __device__ __forceinline__ void down_item(const LoraArgs& a, int64_t t0, uint64_
   __syncthreads();
 }
 
-// Few rows: workgroup (row, share).  The row's workgroup works for all rows of the row's
-// adapter in its tile if it is the first of them, and has nothing to do otherwise.
+// Of the row's lane and the lanes before it in its 16: whether an earlier one has the same id.
+template <int D = 1>
+__device__ __forceinline__ bool seen_before(int id) {
+  if constexpr (D < kTile) {
+    const int before = __builtin_amdgcn_update_dpp(-1, id, 0x110 + D, 0xF, 0xF, false);   // lane - D
+    return (before == id) | seen_before<D + 1>(id);
+  } else {
+    return false;
+  }
+}
+
+// Few rows: an item is the rows of one adapter in a tile of 16, whatever lies between them.
+// Every workgroup finds the items from the ids, and the workgroups are dealt out to them
+// evenly: S workgroups an item, a part of K each.
 template <int RT>
 __global__ void __launch_bounds__(64 * kDownWaves, 2)
 lora_down_rows_kernel(LoraArgs a) {
   __shared__ __attribute__((aligned(16))) float red[down_slots<RT>()][RT][kTile * 16];
-  const int lane = threadIdx.x & 63, at = blockIdx.x & (kTile - 1);
-  const int64_t t0 = blockIdx.x - at, t = t0 + (lane & (kTile - 1));
-  const int id = t < a.T ? a.ids[t] : -1;
-  const int adapter = __builtin_amdgcn_readlane(id, at);
-  const uint64_t rows = __builtin_amdgcn_ballot_w64(id == adapter) & 0xFFFF;
-  if (adapter < 0 || adapter >= a.L || __builtin_ctzll(rows) != at) return;
-  const int pieces = a.K / 64, s = blockIdx.y;
-  down_item<1, RT>(a, t0, rows, adapter, s, (int)((int64_t)pieces * s / a.S),
-                   (int)((int64_t)pieces * (s + 1) / a.S), red);
+  static_assert(kLoraFewRows <= 128, "two rows a lane");
+  const int lane = threadIdx.x & 63;
+  int id[2] = {-1, -1};
+  uint64_t lead[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (a.T <= 64 * i) break;
+    const int t = 64 * i + lane;
+    id[i] = t < a.T ? a.ids[t] : -1;
+    id[i] = id[i] >= 0 && id[i] < a.L ? id[i] : -1;
+    lead[i] = __builtin_amdgcn_ballot_w64((id[i] >= 0) & (a.T == 1 || !seen_before(id[i])));
+  }
+  const uint32_t n0 = __builtin_popcountll(lead[0]), n = n0 + __builtin_popcountll(lead[1]);
+  if (n == 0) return;
+  // quotients of these sizes come out exact (halves are far from the next integer)
+  const uint32_t most = (uint32_t)(((float)gridDim.x + 0.5f) * __builtin_amdgcn_rcpf((float)n));
+  const uint32_t S = most < (uint32_t)a.S ? most : (uint32_t)a.S;
+  const float per = __builtin_amdgcn_rcpf((float)S);
+  const uint32_t item = (uint32_t)(((float)blockIdx.x + 0.5f) * per), s = blockIdx.x - item * S;
+  if (item >= n) return;
+  const bool second = item >= n0;
+  const uint64_t heads = second ? lead[1] : lead[0];
+  const int mine = second ? id[1] : id[0];
+  const uint32_t before = __builtin_amdgcn_mbcnt_hi((uint32_t)(heads >> 32),
+                                                    __builtin_amdgcn_mbcnt_lo((uint32_t)heads, 0));
+  const int at = __builtin_ctzll(
+      __builtin_amdgcn_ballot_w64(((heads >> lane) & 1) && before == item - (second ? n0 : 0)));
+  const int adapter = __builtin_amdgcn_readlane(mine, at), tile = at & ~(kTile - 1);
+  const uint64_t rows = (__builtin_amdgcn_ballot_w64(mine == adapter) >> tile) & 0xFFFF;
+  const int64_t t0 = tile + (second ? 64 : 0);
+  if (s == 0 && threadIdx.x < kTile && ((rows >> threadIdx.x) & 1)) a.parts[t0 + threadIdx.x] = (int)S;
+  const int pieces = a.K / 64;
+  const float share = (float)pieces * per;        // any rounding will do: part s ends where s + 1 begins
+  down_item<1, RT>(a, t0, rows, adapter, (int)s, (int)((float)s * share),
+                   s + 1 == S ? pieces : (int)((float)(s + 1) * share), red);
 }
 
 // Many rows: an item is a run of rows of one adapter within a tile of 16 MT.  Every workgroup
@@ -440,6 +478,9 @@ lora_up_kernel(LoraArgs a) {
   const int64_t t0 = (int64_t)tile * M;
   const int64_t n0 = ((int64_t)(blockIdx.x - back * across) * W + wave) * C;
   TileAdapters<M> ad(a, t0, lane, q, a.up_Q);
+  // parts of the lanes' rows' sums (of rows without an adapter anything: not used)
+  const int64_t t = t0 + (lane & (M - 1));
+  const int lane_parts = a.parts[t < a.T ? t : a.T - 1];
   const uint64_t mine = ad.own | (q == 0 ? ad.none : 0);  // rows that this workgroup writes
   if (!mine) return;
 
@@ -513,9 +554,9 @@ lora_up_kernel(LoraArgs a) {
     float v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+    const int S = __shfl(lane_parts, row, 64);
     if (((ad.own >> row) & 1) && c < a.R) {
       const float* p = a.h + (t0 + row) * a.R + c;
-      const int S = a.parts ? a.parts[t0 + row] : a.S;
       for (int s0 = 0; s0 < S; s0 += 4) {
         float4 x[4], y[4];
 #pragma unroll
@@ -642,7 +683,7 @@ void launch_down(const LoraArgs& a, hipStream_t stream) {
 }
 
 void launch_down_rows(const LoraArgs& a, hipStream_t stream) {
-  const dim3 grid((unsigned)a.T, a.S), block(64 * kDownWaves);
+  const dim3 grid(a.grid), block(64 * kDownWaves);
   if (a.R <= 16) hipLaunchKernelGGL((lora_down_rows_kernel<1>), grid, block, 0, stream, a);
   else if (a.R <= 32) hipLaunchKernelGGL((lora_down_rows_kernel<2>), grid, block, 0, stream, a);
   else if (a.R <= 64) hipLaunchKernelGGL((lora_down_rows_kernel<4>), grid, block, 0, stream, a);
@@ -667,7 +708,11 @@ void lora_plan(LoraArgs* a) {
   auto most = [&](int mt) { return cdiv(K, 512 * (mt + rt <= 2 ? 4 : mt + rt <= 4 ? 2 : 1)); };
   if (T <= kLoraFewRows) {
     a->mt = 0;
-    a->S = (int)(cdiv(256, T) < most(1) ? cdiv(256, T) : most(1));
+    // as many parts as 256 workgroups give the fewest items, but up to 16 only where more rows
+    // read them back (128 x 7168 x 16384 of rank 64, two adapters in a mixed batch: 19.1 us,
+    // 27.5 with 4 at most; a share of K for each row, with an item or not: 44.5)
+    const int64_t S = cdiv(256, T) > 16 ? cdiv(256, T) : 16;
+    a->S = (int)(S < most(1) ? S : most(1));
   } else {
     const int64_t rows = T < kLoraRows ? T : kLoraRows;
     int mt = a->R <= 64 ? 4 : 2;
@@ -675,17 +720,22 @@ void lora_plan(LoraArgs* a) {
     const int64_t S = cdiv(256, cdiv(rows, mt * kTile)) + 1;
     a->mt = mt;
     a->S = (int)(S < most(mt) ? S : most(mt) < 2 ? 2 : most(mt));
-    a->grid = 256;
   }
+  a->grid = a->mt == 0 && T * a->S < 256 ? (int)(T * a->S) : 256;
   // second kernel
   // 64 rows share an adapter's weights where they are many (R > 32), else 32: 4096 x 7168 of
   // rank 16 32.9 us with 64 rows a workgroup, 30.5 with 32; 8192 x 7168 of rank 64 79 and 81
   a->up_mt = a->R <= 32 ? (T <= 64 ? 1 : 2) : T <= 16 ? 1 : 4;
-  const int64_t up_tiles = cdiv(T, a->up_mt * kTile) * cdiv(a->N, a->up_mt == 1 ? 128 : 256);
-  // workgroups on the same rows: those that find nothing to do cost little beside few others
+  // few rows: adapters two at a time in half the columns rather than one by one (100 x 4096 x
+  // 7168, 40 adapters of rank 64: 31.8 us, 32.5 with 64 columns a wave)
   const bool few = T <= kLoraFewRows;
+  a->up_ct = few ? 2 : 4;
+  const int64_t up_tiles = cdiv(T, a->up_mt * kTile) * cdiv(a->N, kUpWaves * kTile * a->up_ct);
+  // workgroups on the same rows: those that find nothing to do cost little beside few others
+  // (128 x 24576 x 1536, ranks up to 64, 8 adapters: 22.9 us for up to 512 workgroups, 21.1 for
+  // 1024, 24.9 for 2048)
   a->up_Q = 1;
-  while (a->up_Q < (few ? 16 : 4) && a->up_Q < T && 2 * a->up_Q * up_tiles <= (few ? 512 : 2048))
+  while (a->up_Q < (few ? 16 : 4) && a->up_Q < T && 2 * a->up_Q * up_tiles <= (few ? 1024 : 2048))
     a->up_Q *= 2;
 }
 
@@ -703,9 +753,19 @@ void launch_lora(const LoraArgs& all, hipStream_t stream) {
     else if (a.mt == 4) launch_down<4>(a, stream);
     else if (a.mt == 2) launch_down<2>(a, stream);
     else launch_down<1>(a, stream);
-    if (a.R <= 32) a.up_mt == 1 ? launch_up<1, 1, 2, 4>(a, stream) : launch_up<2, 1, 4, 2>(a, stream);
-    else if (a.R <= 64) a.up_mt == 1 ? launch_up<1, 2, 2, 2>(a, stream) : launch_up<4, 2, 4, 1>(a, stream);
-    else a.up_mt == 1 ? launch_up<1, 4, 2, 1>(a, stream) : launch_up<4, 4, 4, 1>(a, stream);
+    if (a.R <= 32) {
+      if (a.up_mt == 1) launch_up<1, 1, 2, 4>(a, stream);
+      else if (a.up_ct == 2) launch_up<2, 1, 2, 4>(a, stream);
+      else launch_up<2, 1, 4, 2>(a, stream);
+    } else if (a.R <= 64) {
+      if (a.up_mt == 1) launch_up<1, 2, 2, 2>(a, stream);
+      else if (a.up_ct == 2) launch_up<4, 2, 2, 2>(a, stream);
+      else launch_up<4, 2, 4, 1>(a, stream);
+    } else {
+      if (a.up_mt == 1) launch_up<1, 4, 2, 1>(a, stream);
+      else if (a.up_ct == 2) launch_up<4, 4, 2, 1>(a, stream);
+      else launch_up<4, 4, 4, 1>(a, stream);
+    }
   }
 }
 

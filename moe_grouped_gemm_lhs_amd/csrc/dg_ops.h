@@ -67,15 +67,16 @@ struct LoraArgs {
   int64_t ld_out;
   float* h;                    // S x T x R, the workspace
   int64_t h_part;              // elements from one part to the next
-  int* parts;                  // T, behind it: parts of a row's sums (nullptr: S)
+  int* parts;                  // T, behind it: parts of a row's sums
   int64_t T, N;
   int K, R, L;
   // the plan for the sizes (lora_plan)
   int mt;                      // first kernel: row tiles of 16 a workgroup; 0: the one for
                                // few rows
   int S;                       // parts of the sums over K, at most
-  int grid;                    // workgroups of the kernel for many rows
+  int grid;                    // workgroups of the first kernel
   int up_mt;                   // second kernel: row tiles of 16 a workgroup
+  int up_ct;                   // its column tiles of 16 a wave
   int up_Q;                    // workgroups over the adapters of the same rows
 };
 

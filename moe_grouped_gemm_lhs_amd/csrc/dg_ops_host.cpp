@@ -131,7 +131,7 @@ size_t dg_lora_workspace_bytes(int64_t T, int64_t N, int64_t K, int64_t R, int64
   dg::LoraArgs a{};
   a.T = T; a.N = N; a.K = (int)K; a.R = (int)R;
   dg::lora_plan(&a);
-  return (size_t)a.S * T * R * 4 + (a.mt > 0 ? (size_t)T * 4 : 0);
+  return (size_t)a.S * T * R * 4 + (size_t)T * 4;
 }
 
 dg_status dg_lora_bf16(const uint16_t* X, int64_t ldx, const uint16_t* A, const uint16_t* B,
@@ -160,7 +160,7 @@ dg_status dg_lora_bf16(const uint16_t* X, int64_t ldx, const uint16_t* A, const 
   a.h = (float*)workspace;
   a.T = T; a.N = N; a.K = (int)K; a.R = (int)R; a.L = (int)L;
   dg::lora_plan(&a);
-  if (a.mt > 0) a.parts = (int*)(a.h + (int64_t)a.S * T * R);
+  a.parts = (int*)(a.h + (int64_t)a.S * T * R);
   (void)hipGetLastError();
   dg::launch_lora(a, (hipStream_t)stream);
   return hipGetLastError() == hipSuccess ? DG_OK : DG_ERR_HIP;
