@@ -1,6 +1,7 @@
 """Binding of the gate and the adapters (include/dg.h): dg_moe_route,
 dg_moe_route_backward, dg_lora_bf16, and moe_route, the gate as a differentiable torch
 function.  As in binding.py: argument checks and marshalling, no arithmetic, no fallback.
+The calls and the checks of their usual arguments go through _marshal (csrc/dg_marshal.cpp).
 """
 from __future__ import annotations
 
@@ -13,25 +14,36 @@ from .binding import _IN_DTYPES, DGError, load_library
 DG_SCORE_SOFTMAX, DG_SCORE_SIGMOID = 0, 1
 _SCORES = {"softmax": DG_SCORE_SOFTMAX, "sigmoid": DG_SCORE_SIGMOID}
 _workspaces: dict = {}
+_native = None
+
+
+def _load_native():
+    """_marshal, with libdg (raises if either was not built)."""
+    global _native
+    if _native is None:
+        load_library()
+        try:
+            from . import _marshal
+        except ImportError as e:
+            raise RuntimeError("_marshal.so is missing or does not load: build it with "
+                               "`python -m moe_grouped_gemm_lhs_amd.build`") from e
+        _marshal.use_slow(_vector, _rows)
+        _native = _marshal
+    return _native
 
 
 def dg_moe_route_workspace_bytes(T: int, E: int) -> int:
-    return int(load_library().dg_moe_route_workspace_bytes(T, E))
+    return (_native or _load_native()).dg_moe_route_workspace_bytes(T, E)
 
 
 def dg_lora_workspace_bytes(T: int, N: int, K: int, R: int, L: int) -> int:
-    return int(load_library().dg_lora_workspace_bytes(T, N, K, R, L))
+    return (_native or _load_native()).dg_lora_workspace_bytes(T, N, K, R, L)
 
 
 # ------------------------------------------------------------------------ marshalling
-# A decode step makes these calls once a layer with little for the GPU to do, so the usual
-# case of every check is one expression and what is wrong is found out afterwards.
+# What _marshal's vector() and rows() hand on: arguments that are not the usual ones.
 def _vector(t, name, dtype, shape, device):
     """Pointer of an optional dense argument (None: a null pointer)."""
-    if t is None:
-        return None
-    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
-        return t.data_ptr()
     binding._check(t, name, dtype, shape, device)
     return t.data_ptr()
 
@@ -121,14 +133,15 @@ def dg_moe_route(logits, k, *, bias=None, row_valid=None, score="softmax", norma
     scalar or None, coef E float32 or None): counts with count=True, a counts tensor or a
     balance; loss and coef with a balance.  ids, weights, counts, loss, coef may be given
     to be written in place.  include/dg.h has the formulas."""
+    native = _native or _load_native()
     dev = _logits(logits)
     T, E = logits.shape
     sc = _score(score)
-    p_logits, ld = _rows(logits, "logits", logits.dtype, (T, E), dev)
-    p_bias = _vector(bias, "bias", torch.float32, (E,), dev)
+    p_logits, ld = native.rows(logits, "logits", logits.dtype, (T, E), dev)
+    p_bias = native.vector(bias, "bias", torch.float32, (E,), dev)
     if row_valid is not None and row_valid.dtype is torch.bool:
         row_valid = row_valid.view(torch.uint8)
-    p_valid = _vector(row_valid, "row_valid", torch.uint8, (T,), dev)
+    p_valid = native.vector(row_valid, "row_valid", torch.uint8, (T,), dev)
     if ids is None:
         ids = torch.empty((T, k), dtype=torch.int32, device=dev)
     if weights is None:
@@ -142,17 +155,16 @@ def dg_moe_route(logits, k, *, bias=None, row_valid=None, score="softmax", norma
         raise ValueError("loss and coef need a balance")
     if counts is None and (count or balance is not None):
         counts = torch.empty((E,), dtype=torch.int32, device=dev)
-    p_ids = _vector(ids, "ids", torch.int32, (T, k), dev)
-    p_weights = _vector(weights, "weights", torch.float32, (T, k), dev)
-    p_counts = _vector(counts, "counts", torch.int32, (E,), dev)
-    p_loss = _vector(loss, "loss", torch.float32, (), dev)
-    p_coef = _vector(coef, "coef", torch.float32, (E,), dev)
-    lib = binding._lib or load_library()
+    p_ids = native.vector(ids, "ids", torch.int32, (T, k), dev)
+    p_weights = native.vector(weights, "weights", torch.float32, (T, k), dev)
+    p_counts = native.vector(counts, "counts", torch.int32, (E,), dev)
+    p_loss = native.vector(loss, "loss", torch.float32, (), dev)
+    p_coef = native.vector(coef, "coef", torch.float32, (E,), dev)
     raw = _raw_stream(dev, stream)
     ws, p_ws, ws_bytes = None, None, 0
     if counts is not None:
-        ws, p_ws, ws_bytes = _workspace(lib.dg_moe_route_workspace_bytes(T, E), dev, workspace, stream, raw)
-    st = lib.dg_moe_route(p_logits, _IN_DTYPES[logits.dtype], ld, p_bias, p_valid, T, E, k, sc,
+        ws, p_ws, ws_bytes = _workspace(native.dg_moe_route_workspace_bytes(T, E), dev, workspace, stream, raw)
+    st = native.dg_moe_route(p_logits, _IN_DTYPES[logits.dtype], ld, p_bias, p_valid, T, E, k, sc,
                           bool(normalize), scale, balance or 0.0, p_ids, p_weights, p_counts,
                           p_loss, p_coef, p_ws, ws_bytes, raw)
     if st != 0:
@@ -167,24 +179,25 @@ def dg_moe_route_backward(logits, ids, *, grad_weights=None, coef=None, grad_los
     its weights (T x k float32 or None) and of its loss (coef as returned by the forward
     call, grad_loss a float32 scalar; None: 1).  ids, row_valid, score, normalize and scale
     as in the forward call."""
+    native = _native or _load_native()
     dev = _logits(logits)
     T, E = logits.shape
     if ids.dim() != 2:
         raise ValueError("ids must be 2-D (T x k)")
     k = ids.shape[1]
     sc = _score(score)
-    p_logits, ld = _rows(logits, "logits", logits.dtype, (T, E), dev)
+    p_logits, ld = native.rows(logits, "logits", logits.dtype, (T, E), dev)
     if row_valid is not None and row_valid.dtype is torch.bool:
         row_valid = row_valid.view(torch.uint8)
-    p_valid = _vector(row_valid, "row_valid", torch.uint8, (T,), dev)
-    p_ids = _vector(ids, "ids", torch.int32, (T, k), dev)
-    p_gw = _vector(grad_weights, "grad_weights", torch.float32, (T, k), dev)
-    p_coef = _vector(coef, "coef", torch.float32, (E,), dev)
-    p_gl = _vector(grad_loss, "grad_loss", torch.float32, (), dev)
+    p_valid = native.vector(row_valid, "row_valid", torch.uint8, (T,), dev)
+    p_ids = native.vector(ids, "ids", torch.int32, (T, k), dev)
+    p_gw = native.vector(grad_weights, "grad_weights", torch.float32, (T, k), dev)
+    p_coef = native.vector(coef, "coef", torch.float32, (E,), dev)
+    p_gl = native.vector(grad_loss, "grad_loss", torch.float32, (), dev)
     if grad_logits is None:
         grad_logits = torch.empty((T, E), dtype=logits.dtype, device=dev)
-    p_out, ld_out = _rows(grad_logits, "grad_logits", logits.dtype, (T, E), dev)
-    st = (binding._lib or load_library()).dg_moe_route_backward(
+    p_out, ld_out = native.rows(grad_logits, "grad_logits", logits.dtype, (T, E), dev)
+    st = native.dg_moe_route_backward(
         p_logits, _IN_DTYPES[logits.dtype], ld, p_valid, T, E, k, sc, bool(normalize), scale, p_ids,
         p_gw, p_coef, p_gl, p_out, ld_out, _raw_stream(dev, stream))
     if st != 0:
@@ -234,6 +247,7 @@ def dg_lora_bf16(X, A, B, ids, base=None, out=None, *, scales=None, ranks=None, 
     X (T x K), base and out (T x N) are bfloat16 with rows that may lie apart; A (L x R x
     K) and B (L x N x R) bfloat16; ids (T) int32; scales (L) float32, None: 1; ranks (L)
     int32, None: all R.  base None: zero; out may be base itself.  Returns out."""
+    native = _native or _load_native()
     dev = _device(X, "X")
     if X.dim() != 2 or A.dim() != 3 or B.dim() != 3:
         raise ValueError("X must be 2-D (T x K), A (L x R x K) and B (L x N x R) 3-D")
@@ -241,21 +255,20 @@ def dg_lora_bf16(X, A, B, ids, base=None, out=None, *, scales=None, ranks=None, 
     L, R, _ = A.shape
     N = B.shape[1]
     bf16 = torch.bfloat16
-    p_x, ldx = _rows(X, "X", bf16, (T, K), dev)
-    p_a = _vector(A, "A", bf16, (L, R, K), dev)
-    p_b = _vector(B, "B", bf16, (L, N, R), dev)
-    p_ids = _vector(ids, "ids", torch.int32, (T,), dev)
-    p_s = _vector(scales, "scales", torch.float32, (L,), dev)
-    p_r = _vector(ranks, "ranks", torch.int32, (L,), dev)
-    p_base, ld_base = (None, 0) if base is None else _rows(base, "base", bf16, (T, N), dev)
+    p_x, ldx = native.rows(X, "X", bf16, (T, K), dev)
+    p_a = native.vector(A, "A", bf16, (L, R, K), dev)
+    p_b = native.vector(B, "B", bf16, (L, N, R), dev)
+    p_ids = native.vector(ids, "ids", torch.int32, (T,), dev)
+    p_s = native.vector(scales, "scales", torch.float32, (L,), dev)
+    p_r = native.vector(ranks, "ranks", torch.int32, (L,), dev)
+    p_base, ld_base = (None, 0) if base is None else native.rows(base, "base", bf16, (T, N), dev)
     if out is None:
         out = torch.empty((T, N), dtype=bf16, device=dev)
-    p_out, ld_out = _rows(out, "out", bf16, (T, N), dev)
-    lib = binding._lib or load_library()
+    p_out, ld_out = native.rows(out, "out", bf16, (T, N), dev)
     raw = _raw_stream(dev, stream)
-    ws, p_ws, ws_bytes = _workspace(lib.dg_lora_workspace_bytes(T, N, K, R, L), dev, workspace, stream,
+    ws, p_ws, ws_bytes = _workspace(native.dg_lora_workspace_bytes(T, N, K, R, L), dev, workspace, stream,
                                     raw)
-    st = lib.dg_lora_bf16(p_x, ldx, p_a, p_b, p_ids, p_s, p_r, p_base, ld_base, p_out, ld_out, T, N,
+    st = native.dg_lora_bf16(p_x, ldx, p_a, p_b, p_ids, p_s, p_r, p_base, ld_base, p_out, ld_out, T, N,
                           K, R, L, p_ws, ws_bytes, raw)
     if st != 0:
         raise DGError(st, "dg_lora_bf16")
