@@ -48,7 +48,11 @@ __device__ __forceinline__ uint4 load8(const uint16_t* p) {
   __builtin_memcpy(&v, p, 16);
   return v;
 }
-__device__ __forceinline__ void store8(uint16_t* p, const uint4& v) { __builtin_memcpy(p, &v, 16); }
+__device__ __forceinline__ void store8(uint16_t* p, const uint4& v, bool past_caches) {
+  using u32x4 = __attribute__((ext_vector_type(4), aligned(2))) uint32_t;
+  if (past_caches) __builtin_nontemporal_store(u32x4{v.x, v.y, v.z, v.w}, (u32x4*)p);
+  else __builtin_memcpy(p, &v, 16);
+}
 
 // Lanes eight apart trade: the lower one's y for the upper one's x.  Its own inverse.
 __device__ __forceinline__ void trade(uint4& x, uint4& y, bool upper) {
@@ -326,7 +330,7 @@ lora_down_rows_kernel(LoraArgs a) {
 //    that the run touches, so the single rows of a mixed batch and the ends of prompts
 //    within a tile cost what they cost.
 // An item's parts, at most a.S, are the workgroups that share it; their number goes to
-// `parts` for each of its rows.  8192 x 16384 of rank 64: 85 us, x alone at 3.2 TB/s (a sum over
+// `parts` for each of its rows.  8192 x 16384 of rank 64: 81 us, x alone at 3.3 TB/s (a sum over
 // 512 MB reads 3.9), A again from L2 for each row tile; 4096 x 2048 of rank 16: 9.4.
 constexpr int kCounts = 256;              // blocks of rows, at most
 
@@ -667,7 +671,7 @@ lora_up_kernel(LoraArgs a) {
       if (!((mine >> row) & 1)) continue;
       uint16_t* o = a.out + (t0 + row) * a.ld_out + n;
       if (n + 8 <= a.N) {
-        store8(o, u[p]);
+        store8(o, u[p], a.past_caches);
       } else {
         const uint32_t x[4] = {u[p].x, u[p].y, u[p].z, u[p].w};
 #pragma unroll
@@ -735,6 +739,10 @@ void lora_plan(LoraArgs* a) {
   // 7168, 40 adapters of rank 64: 31.8 us, 32.5 with 64 columns a wave)
   const bool few = T <= kLoraFewRows;
   a->up_ct = few ? 2 : 4;
+  // an output that the caches would hardly hold is not kept in them: 8192 x 7168 (117 MB)
+  // 147.7 us instead of 155.5, 192.6 instead of 197.0 with a copy that reads it next; of 4096
+  // (59 MB) 38.1 instead of 43.8, but 63.5 and 63.2 with the copy
+  a->past_caches = T * a->N * 2 >= kLoraPastCaches;
   const int64_t up_tiles = cdiv(T, a->up_mt * kTile) * cdiv(a->N, kUpWaves * kTile * a->up_ct);
   // workgroups on the same rows: those that find nothing to do cost little beside few others
   // (128 x 24576 x 1536, ranks up to 64, 8 adapters: 22.9 us for up to 512 workgroups, 21.1 for

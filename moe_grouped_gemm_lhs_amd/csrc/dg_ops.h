@@ -52,6 +52,7 @@ void launch_route_backward(const RouteArgs& a, hipStream_t stream);
 constexpr int kLoraMaxR = 128;
 constexpr int64_t kLoraFewRows = 128;
 constexpr int64_t kLoraRows = (int64_t)1 << 20;   // rows of a launch
+constexpr int64_t kLoraPastCaches = (int64_t)96 << 20;   // bytes of an output
 
 struct LoraArgs {
   const uint16_t* x;
@@ -78,6 +79,7 @@ struct LoraArgs {
   int up_mt;                   // second kernel: row tiles of 16 a workgroup
   int up_ct;                   // its column tiles of 16 a wave
   int up_Q;                    // workgroups over the adapters of the same rows
+  bool past_caches;            // out is stored past the caches
 };
 
 void lora_plan(LoraArgs* a);

@@ -160,6 +160,27 @@ def test_more_rows_than_a_launch_takes():
     assert torch.equal(got[none], base[none])
 
 
+@pytest.mark.parametrize("N", [12544, 12301])
+def test_outputs_larger_than_the_caches(N):
+    """Outputs of 100 MB and more are stored past the caches, aligned or not."""
+    T, K, rank, L = 4200, 128, 8, 3
+    p = make(1, N, K, rank, L, 23)
+    x = torch.randn(T, K, device=DEV, dtype=torch.float32).to(BF)
+    base = torch.randn(T, N, device=DEV, dtype=torch.float32).to(BF)
+    ids = ((torch.arange(T, device=DEV) // 700) % (L + 1) - 1).int()
+    A, B = p["A"].to(DEV), p["B"].to(DEV)
+    got = dg.dg_lora_bf16(x, A, B, ids, base)
+    some = torch.arange(1401, device=DEV) * 3                 # the same rows in a smaller call
+    some = some[some < T]
+    assert (got[ids < 0] == base[ids < 0]).all()
+    rows = np.concatenate([np.arange(690, 730), np.arange(T - 40, T)])
+    ref, size = R.lora(host(x[rows]), host(p["A"]), host(p["B"]), ids.cpu().numpy()[rows], None, None,
+                       host(base[rows]))
+    assert np.all(np.abs(host(got[rows]) - ref) <= R.lora_tolerance(ref, size, K))
+    less = dg.dg_lora_bf16(x[some], A, B, ids[some], base[some])
+    assert (got[some].float() - less.float()).abs().max() <= 2.0 ** -7 * got[some].float().abs().max()
+
+
 def test_no_scales_no_base():
     p = make(30, 100, 256, 16, 4, 5)
     check(p, ids_of(30, 4, "mixed"), scales=False)
