@@ -62,7 +62,7 @@ PyObject* vector(PyObject*, PyObject* const* args, Py_ssize_t n) {
 }
 
 // Pointer and row stride of a matrix whose rows are dense but may lie apart.  Of no or one row
-// the stride says nothing.
+// the row stride says nothing.
 PyObject* rows(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (n != 5) {
     PyErr_SetString(PyExc_TypeError, "rows(t, name, dtype, shape, device)");
@@ -71,7 +71,7 @@ PyObject* rows(PyObject*, PyObject* const* args, Py_ssize_t n) {
   try {
     if (matches(args)) {
       const at::Tensor& t = THPVariable_Unpack(args[0]);
-      if (t.dim() == 2 && (t.size(0) <= 1 || t.size(1) <= 1 || t.stride(1) == 1))
+      if (t.dim() == 2 && (t.size(0) == 0 || t.size(1) <= 1 || t.stride(1) == 1))
         return Py_BuildValue("(NL)", PyLong_FromVoidPtr(t.data_ptr()),
                              (long long)(t.size(0) <= 1 ? t.size(1) : t.stride(0)));
     }

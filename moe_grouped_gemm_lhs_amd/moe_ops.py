@@ -52,10 +52,9 @@ def _rows(t, name, dtype, shape, device):
     """Pointer and row stride of a matrix whose rows are dense but may lie apart."""
     if t.dtype is dtype and t.shape == shape and t.device == device:
         ld, one = t.stride()
-        if shape[0] <= 1:                    # no or one row: the stride says nothing
-            return t.data_ptr(), shape[1]
-        if one == 1 or shape[1] <= 1:
-            return t.data_ptr(), ld
+        if shape[0] == 0 or shape[1] <= 1 or one == 1:
+            # of no or one row the row stride says nothing
+            return t.data_ptr(), ld if shape[0] > 1 else shape[1]
         raise ValueError(f"{name} must have dense rows, got strides {(ld, one)}")
     binding._check(t, name, dtype, shape, device)
     raise ValueError(f"{name}: not a matrix this call takes")

@@ -1,0 +1,41 @@
+"""How the calls of the gate and the adapters take their arguments on the GPU: views that they
+refuse."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():  # pragma: no cover
+    pytest.skip("no GPU", allow_module_level=True)
+
+import moe_grouped_gemm_lhs_amd as dg  # noqa: E402
+
+DEV = "cuda:0"
+BF = torch.bfloat16
+
+
+def test_a_row_alone_with_strided_columns_is_refused():
+    """A single token's logits, x, base, out and gradient, as for more rows."""
+    wide = torch.randn(4, 256, device=DEV)
+    z = wide[:1, ::2]
+    ids = torch.zeros(1, 2, dtype=torch.int32, device=DEV)
+    coef = torch.zeros(128, device=DEV)
+    with pytest.raises(ValueError, match="dense rows"):
+        dg.dg_moe_route(z, 2)
+    with pytest.raises(ValueError, match="dense rows"):
+        dg.dg_moe_route_backward(z, ids, coef=coef)
+    with pytest.raises(ValueError, match="dense rows"):
+        dg.dg_moe_route_backward(z.contiguous(), ids, coef=coef, grad_logits=wide[1:2, ::2])
+    xw = torch.randn(4, 256, device=DEV).to(BF)
+    x, strided = xw[:1, :128], xw[:1, ::2]
+    A, B = torch.randn(2, 8, 128, device=DEV).to(BF), torch.randn(2, 128, 8, device=DEV).to(BF)
+    one = torch.zeros(1, dtype=torch.int32, device=DEV)
+    before = xw.clone()
+    for args in ((strided, A, B, one), (x, A, B, one, strided), (x, A, B, one, None, strided)):
+        with pytest.raises(ValueError, match="dense rows"):
+            dg.dg_lora_bf16(*args)
+    assert torch.equal(xw, before)
+    # a row of a wider matrix is dense, whatever its row stride
+    got = dg.dg_lora_bf16(x, A, B, one)
+    assert torch.equal(got, dg.dg_lora_bf16(x.contiguous(), A, B, one))
+    assert torch.equal(dg.dg_moe_route(wide[:1, :128], 2)[0], dg.dg_moe_route(wide[:1, :128].contiguous(), 2)[0])

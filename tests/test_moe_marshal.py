@@ -78,6 +78,28 @@ def test_rows_refusals(native):
         native.rows(None, "t", torch.float32, (6, 9), CPU)
 
 
+@pytest.mark.parametrize("row", [lambda: torch.zeros(6, 10)[:1, ::2], lambda: torch.zeros(6, 10)[:, :1].t(),
+                                 lambda: torch.zeros(1, 1).expand(1, 5)],
+                         ids=["every other column", "a column as a row", "one number repeated"])
+def test_a_row_alone_must_be_dense(native, row):
+    """Of one row only the row stride says nothing; its elements must follow each other."""
+    from moe_grouped_gemm_lhs_amd import moe_ops
+    t = row()
+    assert t.shape[0] == 1 and t.stride(1) != 1
+    for rows in (native.rows, moe_ops._rows):
+        with pytest.raises(ValueError, match="dense rows"):
+            rows(t, "t", torch.float32, tuple(t.shape), CPU)
+
+
+def test_rows_that_hold_nothing_may_have_any_strides(native):
+    from moe_grouped_gemm_lhs_amd import moe_ops
+    t = torch.zeros(6, 10)
+    for rows in (native.rows, moe_ops._rows):
+        assert rows(t[:0, ::2], "t", torch.float32, (0, 5), CPU)[1] == 5
+        assert rows(t.t()[:1, :1], "t", torch.float32, (1, 1), CPU) == (t.data_ptr(), 1)
+        assert rows(t[:1, :0], "t", torch.float32, (1, 0), CPU)[1] == 0
+
+
 def test_calls_convert_their_arguments(native):
     from moe_grouped_gemm_lhs_amd.binding import load_library
     lib = load_library()
