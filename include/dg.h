@@ -259,8 +259,10 @@ dg_status dg_transpose_fp8(const uint8_t *X, uint8_t *Y, int64_t rows, int64_t c
  *
  * With counts the call needs a workspace of dg_moe_route_workspace_bytes bytes (0 for a few
  * rows: none), 16-byte aligned.  It may hold anything before and after the call, so one
- * buffer can serve this call and dg_lora_bf16 in stream order (not two calls that may
- * overlap, and not the GEMM calls, which need theirs zero).
+ * buffer can serve this call and dg_lora_bf16 in stream order, whichever host threads make
+ * the calls: what a call launches is enqueued with nothing of another call with the same
+ * buffer between (not two calls that may overlap on the GPU, not buffers that overlap in
+ * part, and not the GEMM calls, which need theirs zero).
  *
  * Sums over rows are taken in an order that depends on the sizes only: the same inputs give
  * the same bits.  Over several workgroups the loss is added up in multiples of

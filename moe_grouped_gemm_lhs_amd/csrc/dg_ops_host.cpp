@@ -47,6 +47,14 @@ bool route_format(int dtype, int score) {
          (score == DG_SCORE_SOFTMAX || score == DG_SCORE_SIGMOID);
 }
 
+// Held while the launches of a call that meet in its workspace are enqueued: of host threads
+// that share a workspace on a stream, one's launches are then never between another's.  Calls
+// with other workspaces go on meanwhile, but for one in 64.
+std::mutex& workspace_mutex(const void* workspace) {
+  static std::mutex mu[64];
+  return mu[((uintptr_t)workspace >> 8) % 64];
+}
+
 // Rows that can be read or written four elements at a time.
 int route_vec(const void* p, int64_t E, int64_t ld, int bf16) {
   return E % 4 == 0 && ld % 4 == 0 && aligned(p, bf16 ? 8 : 16);
@@ -94,6 +102,8 @@ dg_status dg_moe_route(const void* logits, int dtype, int64_t ld, const float* b
   a.normalize = normalize != 0; a.vec = route_vec(logits, E, ld, bf16);
   a.scale = scale; a.balance = balance; a.ids = ids; a.weights = weights; a.counts = counts;
   a.loss = loss; a.coef = coef; a.workspace = workspace;
+  std::unique_lock<std::mutex> together(workspace_mutex(workspace), std::defer_lock);
+  if (need > 0) together.lock();
   (void)hipGetLastError();
   dg::launch_route(a, (hipStream_t)stream);
   return hipGetLastError() == hipSuccess ? DG_OK : DG_ERR_HIP;
@@ -161,6 +171,7 @@ dg_status dg_lora_bf16(const uint16_t* X, int64_t ldx, const uint16_t* A, const 
   a.T = T; a.N = N; a.K = (int)K; a.R = (int)R; a.L = (int)L;
   dg::lora_plan(&a);
   a.parts = (int*)(a.h + (int64_t)a.S * T * R);
+  std::lock_guard<std::mutex> together(workspace_mutex(workspace));
   (void)hipGetLastError();
   dg::launch_lora(a, (hipStream_t)stream);
   return hipGetLastError() == hipSuccess ? DG_OK : DG_ERR_HIP;

@@ -75,7 +75,8 @@ def _device(t, name):
 def _workspace(need, device, workspace, stream, raw):
     """The caller's workspace, or one kept per (device, launch stream) and grown as needed,
     whatever it holds: the tensor (kept by the caller until the launch), its pointer and
-    size.  Under graph capture each call gets one from the graph's memory."""
+    size.  Threads on one stream share it (the calls keep their launches together).  Under
+    graph capture each call gets one from the graph's memory."""
     if need == 0:
         return None, None, 0
     if workspace is not None:

@@ -1,5 +1,7 @@
 """How the calls of the gate and the adapters take their arguments on the GPU: views that they
-refuse."""
+refuse, threads that share a stream."""
+import threading
+
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -39,3 +41,41 @@ def test_a_row_alone_with_strided_columns_is_refused():
     got = dg.dg_lora_bf16(x, A, B, one)
     assert torch.equal(got, dg.dg_lora_bf16(x.contiguous(), A, B, one))
     assert torch.equal(dg.dg_moe_route(wide[:1, :128], 2)[0], dg.dg_moe_route(wide[:1, :128].contiguous(), 2)[0])
+
+
+def test_threads_on_one_stream():
+    """Threads share the default stream and with it the kept workspace: each call's result is the
+    one it has alone, and of a call of several launches none is between another's."""
+    rng = torch.Generator(device=DEV)
+    rng.manual_seed(3)
+
+    def normal(*shape):
+        return torch.randn(*shape, generator=rng, device=DEV)
+
+    jobs = []
+    for i in range(4):
+        z = normal(3000, 64) * (i + 1)
+        T = (5, 40, 200, 700)[i]
+        x, A, B = normal(T, 512).to(BF), normal(3, 16, 512).to(BF), normal(3, 264, 16).to(BF)
+        ids = (torch.arange(T, device=DEV) % 3).int()
+        jobs.append((lambda z=z: dg.dg_moe_route(z, 4, balance=1.0),
+                     lambda a=(x, A, B, ids): (dg.dg_lora_bf16(*a),)))
+    want = [[f() for f in job] for job in jobs]
+    torch.cuda.synchronize()
+    wrong, start = [], threading.Barrier(len(jobs))
+
+    def work(i):
+        start.wait()
+        got = [[f() for f in jobs[i]] for _ in range(30)]
+        torch.cuda.synchronize()
+        for n, pair in enumerate(got):
+            for w, g in zip(want[i], pair):
+                if not all(torch.equal(a, b) for a, b in zip(w, g)):
+                    wrong.append((i, n))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(jobs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong
