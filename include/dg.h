@@ -238,8 +238,9 @@ dg_status dg_transpose_fp8(const uint8_t *X, uint8_t *Y, int64_t rows, int64_t c
  *            of e.  A key of -inf or NaN is never chosen: a bias of -inf closes an expert;
  *            choices that are left without an expert have id -1 and weight 0.
  *   weights  weights[t][j] = scale * s of the choice, divided, if `normalize` is non-zero,
- *            by the sum of the row's chosen scores (0 where that sum is 0).  The bias is
- *            part of the choice only.
+ *            by the sum of the row's chosen scores.  The quotients keep their precision
+ *            however small the scores are (sigmoid: down to about e^-600; scores below count
+ *            as 0, and 0 / 0 as 0).  The bias is part of the choice only.
  *   row_valid (T bytes or NULL: all rows): a row of 0 is padding.  Its logits may be
  *            anything; its ids are -1, its weights 0, and it is in no count, loss or gradient.
  * and over the rows:

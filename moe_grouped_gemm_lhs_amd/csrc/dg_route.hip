@@ -37,15 +37,60 @@ constexpr float kLog2e = 1.44269504f;
 __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 
 // sigmoid(z) = s and s (1 - s), without cancellation on either side; 0 at -inf, 1 at inf.
-__device__ __forceinline__ float sigmoid(float z, float* slope) {
-  const float e = exp_of(-fabsf(z));
-  const float r = __builtin_amdgcn_rcpf(1.0f + e), er = e * r;
+// Shifted, both times exp(-by): for z up to -18 only, where 1 + exp(z) is 1.
+struct Shift {
+  float by = 0.0f, one = 1.0f;           // one: what exp(z) counts for beside 1
+};
+__device__ __forceinline__ float sigmoid(float z, float* slope, Shift shift = {}) {
+  const float e = exp_of(-fabsf(z) - shift.by);
+  const float r = __builtin_amdgcn_rcpf(__builtin_fmaf(e, shift.one, 1.0f)), er = e * r;
   *slope = r * er;
   return z >= 0.0f ? r : er;
 }
 __device__ __forceinline__ float sigmoid(float z) {
   float slope;
   return sigmoid(z, &slope);
+}
+
+// Scores that leave fp32's range.  Normalized weights and the shares of a sigmoid's row in the
+// loss are quotients of scores, and keep their precision where the scores do not: they are
+// formed from scores relative to the largest of theirs (not below e^-600: sigmoid scores under
+// that or so count as 0).  The sigmoid's in the loss always are.  Otherwise rows with a choice
+// whose score is below kTinyScore, or in the backward pass with sigmoid scores that sum to less
+// than kTinySum (every logit is below -18 then), are done once more.  Ordinary rows have
+// neither, and a ballot leaves both out: done for every row, the first costs 1.5% of a decode
+// step and 2.6% of a backward pass (32768 x 256), the second 8% of one under sigmoid.
+constexpr float kTinyScore = 0x1p-80f, kTinySum = 0x1p-26f;
+
+__device__ __forceinline__ bool any(bool lane) {
+  return __builtin_expect(__builtin_amdgcn_ballot_w64(lane) != 0, 0);
+}
+// Whether it holds in one of the L lanes of this lane's row.
+template <int L>
+__device__ __forceinline__ bool in_row(bool lane) {
+  const uint64_t lanes = __builtin_amdgcn_ballot_w64(lane);
+  if constexpr (L == 64) return lanes != 0;
+  else return ((lanes >> (__lane_id() & ~(L - 1))) & ((1ull << L) - 1)) != 0;
+}
+__device__ __forceinline__ float relative_to(float top) { return fmaxf(fminf(top, 0.0f), -600.0f); }
+__device__ __forceinline__ Shift shift_for(float max) {
+  return max < -18.0f ? Shift{relative_to(max), 0.0f} : Shift{};
+}
+// A choice's score relative to that of the row's choice with the largest logit, and in *rest
+// 1 - s (softmax: 1).
+__device__ __forceinline__ float relative_score(const RouteArgs& a, float z, float top, float* rest) {
+  *rest = 1.0f;
+  if (!a.sigmoid) return exp_of(z - top);
+  const float e = exp_of(-fabsf(z)), r = __builtin_amdgcn_rcpf(1.0f + e);
+  *rest = z >= 0.0f ? e * r : r;
+  return exp_of(fminf(z, 0.0f) - relative_to(top)) * r;
+}
+
+// What the wave's lanes have written to memory is there, and is followed by what they write next.
+__device__ __forceinline__ void wave_memory_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
 }
 
 // ------------------------------------------------------------------------ across lanes
@@ -206,11 +251,16 @@ struct RowNorm {
 };
 
 template <int L, int V>
-__device__ __forceinline__ RowNorm softmax_row(const float (&z)[V], float (&s)[V]) {
+__device__ __forceinline__ float row_max(const float (&z)[V]) {
   float m = z[0];
 #pragma unroll
   for (int v = 1; v < V; ++v) m = fmaxf(m, z[v]);
-  m = group_max<L>(m);
+  return group_max<L>(m);
+}
+
+template <int L, int V>
+__device__ __forceinline__ RowNorm softmax_row(const float (&z)[V], float (&s)[V]) {
+  float m = row_max<L, V>(z);
   const bool none = m == -INFINITY;
   m = none ? 0.0f : m;
   float sum = 0.0f;
@@ -312,10 +362,11 @@ route_kernel(RouteArgs a) {
     if (!a.sigmoid) {
       n = softmax_row<L, V>(z, s);
     } else if (a.loss) {
-      float sum = 0.0f;
+      const Shift shift = shift_for(row_max<L, V>(z));
+      float sum = 0.0f, slope;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        s[v] = sigmoid(z[v]);
+        s[v] = sigmoid(z[v], &slope, shift);
         sum += s[v];
       }
       sum = group_sum<L>(sum);
@@ -345,6 +396,22 @@ route_kernel(RouteArgs a) {
     }
     float f = a.scale;
     if (a.normalize) {
+      bool low = false;
+#pragma unroll
+      for (int q = 0; q < KP; ++q) low = low || (ids[q] >= 0 && w[q] < kTinyScore);
+      // under softmax without a bias the largest logit is a choice's
+      if ((a.bias || a.sigmoid) && any(low)) {
+        low = in_row<L>(low);
+        float top = -INFINITY, rest;
+#pragma unroll
+        for (int q = 0; q < KP; ++q)
+          if (ids[q] >= 0) top = fmaxf(top, load_one(a.logits, at * a.ld + ids[q], a.bf16));
+        top = group_max<L>(top);
+#pragma unroll
+        for (int q = 0; q < KP; ++q)
+          if (low && ids[q] >= 0)
+            w[q] = relative_score(a, load_one(a.logits, at * a.ld + ids[q], a.bf16), top, &rest);
+      }
       // in pairs, pairs of pairs ... of the choices, whatever L is
       float part[KP];
 #pragma unroll
@@ -498,6 +565,73 @@ static_assert(kRouteMaxGrid <= kSumThreads, "one thread a workgroup's live rows"
 static_assert((kRouteMaxE + kSumMinCols - 1) / kSumMinCols <= 64, "arrivals");
 
 // ----------------------------------------------------------------------------- backward
+// A row with tiny scores, its loss's part from n and us under softmax.  With q the normalized
+// weights over their factor and g their gradients times it, a choice's part of dz is
+// q (g - sum of g q), times 1 - s under sigmoid.
+template <int L>
+__device__ __forceinline__ void tiny_row(const RouteArgs& a, int64_t row, int l, float g_loss, RowNorm n,
+                                         float us) {
+  const int64_t at = row * a.ld;
+  auto logit = [&](int e) { return load_one(a.logits, at + e, a.bf16); };
+  auto of_loss = [&](int e) { return a.coef ? g_loss * a.coef[e] : 0.0f; };
+  Shift shift;
+  if (a.sigmoid) {
+    float max = -INFINITY, sum = 0.0f, c;
+    us = 0.0f;
+#pragma unroll 1
+    for (int e = l; e < a.E; e += L) max = fmaxf(max, logit(e));
+    shift = shift_for(group_max<L>(max));
+#pragma unroll 1
+    for (int e = l; e < a.E; e += L) {
+      const float s = sigmoid(logit(e), &c, shift);
+      sum += s;
+      us = __builtin_fmaf(of_loss(e), s, us);
+    }
+    sum = group_sum<L>(sum);
+    n.inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    us = group_sum<L>(us) * n.inv;
+  }
+  // f(expert, its logit, its weight's gradient) for the row's choices
+  auto each = [&](auto f) {
+    if (!a.grad_weights) return;
+#pragma unroll 1
+    for (int j = 0; j < a.k; ++j) {
+      const int e = a.ids_in[row * a.k + j];
+      if (e >= 0 && e < a.E) f(e, logit(e), a.scale * a.grad_weights[row * a.k + j]);
+    }
+  };
+  float top = -INFINITY, total = 0.0f, dot = 0.0f, rest;
+  each([&](int, float x, float) { top = fmaxf(top, x); });
+  each([&](int, float x, float g) {
+    const float s = relative_score(a, x, top, &rest);
+    total += s;
+    dot = __builtin_fmaf(g, s, dot);
+  });
+  const float it = total == 0.0f ? 0.0f : 1.0f / total, mean = dot * it;
+#pragma unroll 1
+  for (int e = l; e < a.E; e += L) {
+    float dz, c;
+    if (a.sigmoid) {
+      sigmoid(logit(e), &c, shift);
+      dz = (of_loss(e) - us) * n.inv * c;
+    } else {
+      dz = exp_of(logit(e) - n.max) * n.inv * (of_loss(e) - us);
+    }
+    each([&](int chosen, float x, float g) {
+      if (chosen != e) return;
+      if (a.normalize) {
+        const float q = relative_score(a, x, top, &rest) * it;
+        dz += q * (g - mean) * rest;
+      } else {                                  // under sigmoid only
+        sigmoid(x, &c);
+        dz += g * c;
+      }
+    });
+    if (a.bf16) ((uint16_t*)a.grad_logits)[row * a.ld_grad + e] = (uint16_t)pack_bf16(dz, 0.0f);
+    else ((float*)a.grad_logits)[row * a.ld_grad + e] = dz;
+  }
+}
+
 // dz from the weights' gradients and the loss's (coef, the same for every row).  A row's
 // scores go through a row of LDS, where the lanes that keep its choices pick theirs up, and
 // the choices' score gradients through another, which is zero but for them.  A wave's next
@@ -558,6 +692,7 @@ route_backward_kernel(RouteArgs a) {
 
     RowNorm n{0.0f, 0.0f};
     float us = 0.0f;                              // sum of u p over the row
+    bool tiny = false;                            // to be done by tiny_row
     if (a.sigmoid) {
       float sum = 0.0f;
 #pragma unroll
@@ -567,6 +702,7 @@ route_backward_kernel(RouteArgs a) {
         us = __builtin_fmaf(u[v], s[v], us);
       }
       sum = group_sum<L>(sum);
+      tiny = live && a.coef && sum < kTinySum;
       n.inv = sum == 0.0f ? 0.0f : 1.0f / sum;
       us = group_sum<L>(us) * n.inv;
     } else {
@@ -597,7 +733,10 @@ route_backward_kernel(RouteArgs a) {
         const float it = total == 0.0f ? 0.0f : 1.0f / total;
         const float mean = dot * it;
 #pragma unroll
-        for (int q = 0; q < KP; ++q) g[q] = (g[q] - mean) * it;
+        for (int q = 0; q < KP; ++q) {
+          tiny = tiny || (chosen[q] >= 0 && sc[q] < kTinyScore);
+          g[q] = (g[q] - mean) * it;
+        }
       }
 #pragma unroll
       for (int q = 0; q < KP; ++q)
@@ -649,6 +788,10 @@ route_backward_kernel(RouteArgs a) {
             }
         }
       }
+    }
+    if (any(tiny)) {
+      wave_memory_sync();
+      if (in_row<L>(tiny)) tiny_row<L>(a, row, l, g_loss, n, us);
     }
   }
 }
