@@ -26,6 +26,7 @@
  * Conventions shared by every call:
  *   - Memory: every pointer is a DEVICE pointer owned by the caller.  The library
  *     allocates and frees nothing.  C is an output the library writes in place.
+ *     Pointers and stream belong to the current device, on which the call launches.
  *   - Layouts (all row-major, densely packed):
  *       A  e4m3fn bytes,   rows x K         sA fp32, rows x (K/128)
  *       B  e4m3fn bytes,   G x N x K        sB fp32, G x ceil(N/128) x (K/128)

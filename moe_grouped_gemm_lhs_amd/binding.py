@@ -138,6 +138,14 @@ def _check(t: torch.Tensor, name: str, dtype, shape, device):
         raise ValueError(f"{name} must be on {device}, got {t.device}")
 
 
+def _elsewhere(device):
+    """The context to make a call in if its tensors are not on the current device (the C calls
+    launch on that, and the null stream is its own on every device), else None."""
+    if device.type == "cuda" and device.index != torch._C._cuda_getDevice():
+        return torch.cuda.device(device)
+    return None
+
+
 def _ptr(t):
     return ctypes.c_void_p(t.data_ptr()) if t is not None else None
 
@@ -183,6 +191,11 @@ def dg_gemm_fp8_nt(A, sA, B, sB, C=None, *, a_format=None, b_format=None, worksp
     """Dense C (M x N bf16) = A (M x K fp8) x B (N x K fp8)^T with block scales.  The
     operand formats come from float8 dtypes, or a_format / b_format ('e4m3', 'e5m2')
     for uint8 bytes (default E4M3); any non-E4M3 operand goes through the _ex call."""
+    there = _elsewhere(A.device)
+    if there is not None:
+        with there:
+            return dg_gemm_fp8_nt(A, sA, B, sB, C, a_format=a_format, b_format=b_format,
+                                  workspace=workspace, stream=stream)
     (A, fa), (B, fb) = _bytes_view(A, "A", a_format), _bytes_view(B, "B", b_format)
     M, K = A.shape
     N = B.shape[0]
@@ -212,6 +225,10 @@ def dg_gemm_fp8_nt(A, sA, B, sB, C=None, *, a_format=None, b_format=None, worksp
 def dg_gemm_fp8_nt_noalloc(A, sA, B, sB, C=None, *, stream=None):
     """dg_gemm_fp8_nt without a workspace argument: split-K calls use the library's
     static per-GPU workspace (calls that overlap on one GPU race).  E4M3 operands."""
+    there = _elsewhere(A.device)
+    if there is not None:
+        with there:
+            return dg_gemm_fp8_nt_noalloc(A, sA, B, sB, C, stream=stream)
     (A, fa), (B, fb) = _bytes_view(A, "A"), _bytes_view(B, "B")
     if fa != DG_FP8_E4M3 or fb != DG_FP8_E4M3:
         raise ValueError("dg_gemm_fp8_nt_noalloc takes E4M3 operands")
@@ -237,6 +254,11 @@ def dg_grouped_gemm_fp8_contiguous(A, sA, B, sB, group_idx, C=None, *, a_format=
                                    b_format=None, workspace=None, stream=None):
     """Contiguous grouped GEMM: A (M_total x K), B (G x N x K), group_idx (M_total int32);
     operand formats as for dg_gemm_fp8_nt."""
+    there = _elsewhere(A.device)
+    if there is not None:
+        with there:
+            return dg_grouped_gemm_fp8_contiguous(A, sA, B, sB, group_idx, C, a_format=a_format,
+                                                  b_format=b_format, workspace=workspace, stream=stream)
     (A, fa), (B, fb) = _bytes_view(A, "A", a_format), _bytes_view(B, "B", b_format)
     M, K = A.shape
     G, N = B.shape[0], B.shape[1]
@@ -270,6 +292,11 @@ def dg_grouped_gemm_fp8_masked(A, sA, B, sB, masked_m, C=None, *, a_format=None,
                                b_format=None, workspace=None, stream=None):
     """Masked grouped GEMM: A (G x cap x K), B (G x N x K), masked_m (G int32); operand
     formats as for dg_gemm_fp8_nt."""
+    there = _elsewhere(A.device)
+    if there is not None:
+        with there:
+            return dg_grouped_gemm_fp8_masked(A, sA, B, sB, masked_m, C, a_format=a_format,
+                                              b_format=b_format, workspace=workspace, stream=stream)
     (A, fa), (B, fb) = _bytes_view(A, "A", a_format), _bytes_view(B, "B", b_format)
     G, cap, K = A.shape
     N = B.shape[1]
@@ -305,6 +332,10 @@ _FP8_OF = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
 
 
 def _quantize(call, X, fmt, scale_rows, Q, S, stream):
+    there = _elsewhere(X.device)
+    if there is not None:
+        with there:
+            return _quantize(call, X, fmt, scale_rows, Q, S, stream)
     if fmt not in _FORMATS:
         raise ValueError(f"unknown fp8 format {fmt!r}")
     if X.dtype not in _IN_DTYPES:
@@ -344,6 +375,10 @@ def dg_quantize_fp8_128x128(X, fmt="e4m3", Q=None, S=None, *, stream=None):
 def dg_transpose_fp8(X, Y=None, *, stream=None):
     """Y (cols x rows) = X (rows x cols)^T for a byte / fp8 matrix on the GPU (rows and
     cols multiples of 16).  Y keeps X's dtype."""
+    there = _elsewhere(X.device)
+    if there is not None:
+        with there:
+            return dg_transpose_fp8(X, Y, stream=stream)
     if X.dim() != 2:
         raise ValueError("X must be 2-D")
     Xb = X.view(torch.uint8) if X.dtype in _FP8_DTYPES else X

@@ -135,6 +135,12 @@ def dg_moe_route(logits, k, *, bias=None, row_valid=None, score="softmax", norma
     to be written in place.  include/dg.h has the formulas."""
     native = _native or _load_native()
     dev = _logits(logits)
+    if dev.index != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            return dg_moe_route(logits, k, bias=bias, row_valid=row_valid, score=score,
+                                normalize=normalize, scale=scale, balance=balance, count=count,
+                                ids=ids, weights=weights, counts=counts, loss=loss, coef=coef,
+                                workspace=workspace, stream=stream)
     T, E = logits.shape
     sc = _score(score)
     p_logits, ld = native.rows(logits, "logits", logits.dtype, (T, E), dev)
@@ -181,6 +187,12 @@ def dg_moe_route_backward(logits, ids, *, grad_weights=None, coef=None, grad_los
     as in the forward call."""
     native = _native or _load_native()
     dev = _logits(logits)
+    if dev.index != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            return dg_moe_route_backward(logits, ids, grad_weights=grad_weights, coef=coef,
+                                         grad_loss=grad_loss, row_valid=row_valid, score=score,
+                                         normalize=normalize, scale=scale, grad_logits=grad_logits,
+                                         stream=stream)
     T, E = logits.shape
     if ids.dim() != 2:
         raise ValueError("ids must be 2-D (T x k)")
@@ -249,6 +261,10 @@ def dg_lora_bf16(X, A, B, ids, base=None, out=None, *, scales=None, ranks=None, 
     int32, None: all R.  base None: zero; out may be base itself.  Returns out."""
     native = _native or _load_native()
     dev = _device(X, "X")
+    if dev.index != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            return dg_lora_bf16(X, A, B, ids, base, out, scales=scales, ranks=ranks,
+                                workspace=workspace, stream=stream)
     if X.dim() != 2 or A.dim() != 3 or B.dim() != 3:
         raise ValueError("X must be 2-D (T x K), A (L x R x K) and B (L x N x R) 3-D")
     T, K = X.shape
