@@ -138,9 +138,15 @@ def _check(t: torch.Tensor, name: str, dtype, shape, device):
         raise ValueError(f"{name} must be on {device}, got {t.device}")
 
 
-def _elsewhere(device):
-    """The context to make a call in if its tensors are not on the current device (the C calls
-    launch on that, and the null stream is its own on every device), else None."""
+def _elsewhere(device, stream):
+    """The context to make a call in, None if that is the present one.  The C calls launch on the
+    current device, which has to be the tensors', and what a call allocates (outputs, zero
+    filled ones among them, and workspace) is ordered before its launch by the current stream,
+    which has to be the one that is given."""
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+        return torch.cuda.stream(stream)
     if device.type == "cuda" and device.index != torch._C._cuda_getDevice():
         return torch.cuda.device(device)
     return None
@@ -150,14 +156,10 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr()) if t is not None else None
 
 
-def _stream(device, stream):
-    """The launch stream as the hipStream_t handle the C calls take."""
-    return ctypes.c_void_p(_launch_stream(device, stream).cuda_stream)
-
-
-def _launch_stream(device, stream):
-    """The stream the call runs on: the one given, else the device's current stream."""
-    return stream if stream is not None else torch.cuda.current_stream(device)
+def _stream(device):
+    """The device's current stream, which a call runs on, as the hipStream_t handle the C calls
+    take."""
+    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
 def _workspace(kind, rows, N, K, G, device, workspace, stream):
@@ -191,11 +193,11 @@ def dg_gemm_fp8_nt(A, sA, B, sB, C=None, *, a_format=None, b_format=None, worksp
     """Dense C (M x N bf16) = A (M x K fp8) x B (N x K fp8)^T with block scales.  The
     operand formats come from float8 dtypes, or a_format / b_format ('e4m3', 'e5m2')
     for uint8 bytes (default E4M3); any non-E4M3 operand goes through the _ex call."""
-    there = _elsewhere(A.device)
+    there = _elsewhere(A.device, stream)
     if there is not None:
         with there:
             return dg_gemm_fp8_nt(A, sA, B, sB, C, a_format=a_format, b_format=b_format,
-                                  workspace=workspace, stream=stream)
+                                  workspace=workspace)
     (A, fa), (B, fb) = _bytes_view(A, "A", a_format), _bytes_view(B, "B", b_format)
     M, K = A.shape
     N = B.shape[0]
@@ -208,7 +210,7 @@ def dg_gemm_fp8_nt(A, sA, B, sB, C=None, *, a_format=None, b_format=None, worksp
     if C is None:
         C = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
     _check(C, "C", torch.bfloat16, (M, N), dev)
-    st_ = _launch_stream(dev, stream)
+    st_ = torch.cuda.current_stream(dev)
     ws, wsb = _workspace(DG_DENSE, M, N, K, 1, dev, workspace, st_)
     lib = load_library()
     if fa == DG_FP8_E4M3 and fb == DG_FP8_E4M3:
@@ -225,10 +227,10 @@ def dg_gemm_fp8_nt(A, sA, B, sB, C=None, *, a_format=None, b_format=None, worksp
 def dg_gemm_fp8_nt_noalloc(A, sA, B, sB, C=None, *, stream=None):
     """dg_gemm_fp8_nt without a workspace argument: split-K calls use the library's
     static per-GPU workspace (calls that overlap on one GPU race).  E4M3 operands."""
-    there = _elsewhere(A.device)
+    there = _elsewhere(A.device, stream)
     if there is not None:
         with there:
-            return dg_gemm_fp8_nt_noalloc(A, sA, B, sB, C, stream=stream)
+            return dg_gemm_fp8_nt_noalloc(A, sA, B, sB, C)
     (A, fa), (B, fb) = _bytes_view(A, "A"), _bytes_view(B, "B")
     if fa != DG_FP8_E4M3 or fb != DG_FP8_E4M3:
         raise ValueError("dg_gemm_fp8_nt_noalloc takes E4M3 operands")
@@ -244,7 +246,7 @@ def dg_gemm_fp8_nt_noalloc(A, sA, B, sB, C=None, *, stream=None):
         C = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
     _check(C, "C", torch.bfloat16, (M, N), dev)
     st = load_library().dg_gemm_fp8_nt_noalloc(_ptr(A), _ptr(sA), _ptr(B), _ptr(sB), _ptr(C),
-                                               M, N, K, _stream(dev, stream))
+                                               M, N, K, _stream(dev))
     if st != 0:
         raise DGError(st, "dg_gemm_fp8_nt_noalloc")
     return C
@@ -254,11 +256,11 @@ def dg_grouped_gemm_fp8_contiguous(A, sA, B, sB, group_idx, C=None, *, a_format=
                                    b_format=None, workspace=None, stream=None):
     """Contiguous grouped GEMM: A (M_total x K), B (G x N x K), group_idx (M_total int32);
     operand formats as for dg_gemm_fp8_nt."""
-    there = _elsewhere(A.device)
+    there = _elsewhere(A.device, stream)
     if there is not None:
         with there:
             return dg_grouped_gemm_fp8_contiguous(A, sA, B, sB, group_idx, C, a_format=a_format,
-                                                  b_format=b_format, workspace=workspace, stream=stream)
+                                                  b_format=b_format, workspace=workspace)
     (A, fa), (B, fb) = _bytes_view(A, "A", a_format), _bytes_view(B, "B", b_format)
     M, K = A.shape
     G, N = B.shape[0], B.shape[1]
@@ -272,7 +274,7 @@ def dg_grouped_gemm_fp8_contiguous(A, sA, B, sB, group_idx, C=None, *, a_format=
     if C is None:
         C = torch.zeros((M, N), dtype=torch.bfloat16, device=dev)
     _check(C, "C", torch.bfloat16, (M, N), dev)
-    st_ = _launch_stream(dev, stream)
+    st_ = torch.cuda.current_stream(dev)
     ws, wsb = _workspace(DG_CONTIGUOUS, M, N, K, G, dev, workspace, st_)
     lib = load_library()
     if fa == DG_FP8_E4M3 and fb == DG_FP8_E4M3:
@@ -292,11 +294,11 @@ def dg_grouped_gemm_fp8_masked(A, sA, B, sB, masked_m, C=None, *, a_format=None,
                                b_format=None, workspace=None, stream=None):
     """Masked grouped GEMM: A (G x cap x K), B (G x N x K), masked_m (G int32); operand
     formats as for dg_gemm_fp8_nt."""
-    there = _elsewhere(A.device)
+    there = _elsewhere(A.device, stream)
     if there is not None:
         with there:
             return dg_grouped_gemm_fp8_masked(A, sA, B, sB, masked_m, C, a_format=a_format,
-                                              b_format=b_format, workspace=workspace, stream=stream)
+                                              b_format=b_format, workspace=workspace)
     (A, fa), (B, fb) = _bytes_view(A, "A", a_format), _bytes_view(B, "B", b_format)
     G, cap, K = A.shape
     N = B.shape[1]
@@ -310,7 +312,7 @@ def dg_grouped_gemm_fp8_masked(A, sA, B, sB, masked_m, C=None, *, a_format=None,
     if C is None:
         C = torch.zeros((G, cap, N), dtype=torch.bfloat16, device=dev)
     _check(C, "C", torch.bfloat16, (G, cap, N), dev)
-    st_ = _launch_stream(dev, stream)
+    st_ = torch.cuda.current_stream(dev)
     ws, wsb = _workspace(DG_MASKED, cap, N, K, G, dev, workspace, st_)
     lib = load_library()
     if fa == DG_FP8_E4M3 and fb == DG_FP8_E4M3:
@@ -332,10 +334,10 @@ _FP8_OF = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
 
 
 def _quantize(call, X, fmt, scale_rows, Q, S, stream):
-    there = _elsewhere(X.device)
+    there = _elsewhere(X.device, stream)
     if there is not None:
         with there:
-            return _quantize(call, X, fmt, scale_rows, Q, S, stream)
+            return _quantize(call, X, fmt, scale_rows, Q, S, None)
     if fmt not in _FORMATS:
         raise ValueError(f"unknown fp8 format {fmt!r}")
     if X.dtype not in _IN_DTYPES:
@@ -354,7 +356,7 @@ def _quantize(call, X, fmt, scale_rows, Q, S, stream):
         S = torch.empty((scale_rows, K // 128), dtype=torch.float32, device=dev)
     _check(S, "S", torch.float32, (scale_rows, K // 128), dev)
     st = getattr(load_library(), call)(_ptr(X), _IN_DTYPES[X.dtype], _ptr(Qb), _ptr(S), rows,
-                                       K, _FORMATS[fmt], _stream(dev, stream))
+                                       K, _FORMATS[fmt], _stream(dev))
     if st != 0:
         raise DGError(st, call)
     return Qb.view(_FP8_OF[fmt]), S
@@ -375,10 +377,10 @@ def dg_quantize_fp8_128x128(X, fmt="e4m3", Q=None, S=None, *, stream=None):
 def dg_transpose_fp8(X, Y=None, *, stream=None):
     """Y (cols x rows) = X (rows x cols)^T for a byte / fp8 matrix on the GPU (rows and
     cols multiples of 16).  Y keeps X's dtype."""
-    there = _elsewhere(X.device)
+    there = _elsewhere(X.device, stream)
     if there is not None:
         with there:
-            return dg_transpose_fp8(X, Y, stream=stream)
+            return dg_transpose_fp8(X, Y)
     if X.dim() != 2:
         raise ValueError("X must be 2-D")
     Xb = X.view(torch.uint8) if X.dtype in _FP8_DTYPES else X
@@ -391,7 +393,7 @@ def dg_transpose_fp8(X, Y=None, *, stream=None):
         Y = torch.empty((cols, rows), dtype=X.dtype, device=dev)
     Yb = Y.view(torch.uint8) if Y.dtype in _FP8_DTYPES else Y
     _check(Yb, "Y", torch.uint8, (cols, rows), dev)
-    st = load_library().dg_transpose_fp8(_ptr(Xb), _ptr(Yb), rows, cols, _stream(dev, stream))
+    st = load_library().dg_transpose_fp8(_ptr(Xb), _ptr(Yb), rows, cols, _stream(dev))
     if st != 0:
         raise DGError(st, "dg_transpose_fp8")
     return Y

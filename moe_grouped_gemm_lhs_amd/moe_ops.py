@@ -60,19 +60,13 @@ def _rows(t, name, dtype, shape, device):
     raise ValueError(f"{name}: not a matrix this call takes")
 
 
-def _raw_stream(device, stream):
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(device.index)
-
-
 def _device(t, name):
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a GPU, got {t.device}")
     return t.device
 
 
-def _workspace(need, device, workspace, stream, raw):
+def _workspace(need, device, workspace, raw):
     """The caller's workspace, or one kept per (device, launch stream) and grown as needed,
     whatever it holds: the tensor (kept by the caller until the launch), its pointer and
     size.  Threads on one stream share it (the calls keep their launches together).  Under
@@ -85,21 +79,17 @@ def _workspace(need, device, workspace, stream, raw):
         return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
     key = (device.index, raw)
     kept = _workspaces.get(key)
-    enough = kept is not None and kept[2] >= need
-    if enough and stream is None and not torch.cuda.is_current_stream_capturing():
+    capturing = torch.cuda.is_current_stream_capturing()
+    if kept is not None and kept[2] >= need and not capturing:
         return kept
-    st = stream if stream is not None else torch.cuda.current_stream(device)
-    with torch.cuda.stream(st):
-        capturing = torch.cuda.is_current_stream_capturing()
-        if enough and not capturing:
-            return kept
-        ws = torch.empty(max(need, 1 << 16), dtype=torch.uint8, device=device)
-        if not capturing:
-            # a smaller one was used on this stream only, so the allocator may hand its
-            # memory out again in this stream's order
-            with binding._lock:
-                _workspaces[key] = (ws, ws.data_ptr(), ws.numel())
-    return ws, ws.data_ptr(), ws.numel()
+    ws = torch.empty(max(need, 1 << 16), dtype=torch.uint8, device=device)
+    kept = ws, ws.data_ptr(), ws.numel()
+    if not capturing:
+        # a smaller one was used on this stream only, so the allocator may hand its memory out
+        # again in this stream's order
+        with binding._lock:
+            _workspaces[key] = kept
+    return kept
 
 
 def _score(score):
@@ -135,12 +125,12 @@ def dg_moe_route(logits, k, *, bias=None, row_valid=None, score="softmax", norma
     to be written in place.  include/dg.h has the formulas."""
     native = _native or _load_native()
     dev = _logits(logits)
-    if dev.index != torch._C._cuda_getDevice():
-        with torch.cuda.device(dev):
+    if stream is not None or dev.index != torch._C._cuda_getDevice():
+        with binding._elsewhere(dev, stream):
             return dg_moe_route(logits, k, bias=bias, row_valid=row_valid, score=score,
                                 normalize=normalize, scale=scale, balance=balance, count=count,
                                 ids=ids, weights=weights, counts=counts, loss=loss, coef=coef,
-                                workspace=workspace, stream=stream)
+                                workspace=workspace)
     T, E = logits.shape
     sc = _score(score)
     p_logits, ld = native.rows(logits, "logits", logits.dtype, (T, E), dev)
@@ -166,10 +156,10 @@ def dg_moe_route(logits, k, *, bias=None, row_valid=None, score="softmax", norma
     p_counts = native.vector(counts, "counts", torch.int32, (E,), dev)
     p_loss = native.vector(loss, "loss", torch.float32, (), dev)
     p_coef = native.vector(coef, "coef", torch.float32, (E,), dev)
-    raw = _raw_stream(dev, stream)
+    raw = torch._C._cuda_getCurrentRawStream(dev.index)
     ws, p_ws, ws_bytes = None, None, 0
     if counts is not None:
-        ws, p_ws, ws_bytes = _workspace(native.dg_moe_route_workspace_bytes(T, E), dev, workspace, stream, raw)
+        ws, p_ws, ws_bytes = _workspace(native.dg_moe_route_workspace_bytes(T, E), dev, workspace, raw)
     st = native.dg_moe_route(p_logits, _IN_DTYPES[logits.dtype], ld, p_bias, p_valid, T, E, k, sc,
                           bool(normalize), scale, balance or 0.0, p_ids, p_weights, p_counts,
                           p_loss, p_coef, p_ws, ws_bytes, raw)
@@ -187,12 +177,11 @@ def dg_moe_route_backward(logits, ids, *, grad_weights=None, coef=None, grad_los
     as in the forward call."""
     native = _native or _load_native()
     dev = _logits(logits)
-    if dev.index != torch._C._cuda_getDevice():
-        with torch.cuda.device(dev):
+    if stream is not None or dev.index != torch._C._cuda_getDevice():
+        with binding._elsewhere(dev, stream):
             return dg_moe_route_backward(logits, ids, grad_weights=grad_weights, coef=coef,
                                          grad_loss=grad_loss, row_valid=row_valid, score=score,
-                                         normalize=normalize, scale=scale, grad_logits=grad_logits,
-                                         stream=stream)
+                                         normalize=normalize, scale=scale, grad_logits=grad_logits)
     T, E = logits.shape
     if ids.dim() != 2:
         raise ValueError("ids must be 2-D (T x k)")
@@ -211,7 +200,7 @@ def dg_moe_route_backward(logits, ids, *, grad_weights=None, coef=None, grad_los
     p_out, ld_out = native.rows(grad_logits, "grad_logits", logits.dtype, (T, E), dev)
     st = native.dg_moe_route_backward(
         p_logits, _IN_DTYPES[logits.dtype], ld, p_valid, T, E, k, sc, bool(normalize), scale, p_ids,
-        p_gw, p_coef, p_gl, p_out, ld_out, _raw_stream(dev, stream))
+        p_gw, p_coef, p_gl, p_out, ld_out, torch._C._cuda_getCurrentRawStream(dev.index))
     if st != 0:
         raise DGError(st, "dg_moe_route_backward")
     return grad_logits
@@ -261,10 +250,10 @@ def dg_lora_bf16(X, A, B, ids, base=None, out=None, *, scales=None, ranks=None, 
     int32, None: all R.  base None: zero; out may be base itself.  Returns out."""
     native = _native or _load_native()
     dev = _device(X, "X")
-    if dev.index != torch._C._cuda_getDevice():
-        with torch.cuda.device(dev):
+    if stream is not None or dev.index != torch._C._cuda_getDevice():
+        with binding._elsewhere(dev, stream):
             return dg_lora_bf16(X, A, B, ids, base, out, scales=scales, ranks=ranks,
-                                workspace=workspace, stream=stream)
+                                workspace=workspace)
     if X.dim() != 2 or A.dim() != 3 or B.dim() != 3:
         raise ValueError("X must be 2-D (T x K), A (L x R x K) and B (L x N x R) 3-D")
     T, K = X.shape
@@ -281,9 +270,8 @@ def dg_lora_bf16(X, A, B, ids, base=None, out=None, *, scales=None, ranks=None, 
     if out is None:
         out = torch.empty((T, N), dtype=bf16, device=dev)
     p_out, ld_out = native.rows(out, "out", bf16, (T, N), dev)
-    raw = _raw_stream(dev, stream)
-    ws, p_ws, ws_bytes = _workspace(native.dg_lora_workspace_bytes(T, N, K, R, L), dev, workspace, stream,
-                                    raw)
+    raw = torch._C._cuda_getCurrentRawStream(dev.index)
+    ws, p_ws, ws_bytes = _workspace(native.dg_lora_workspace_bytes(T, N, K, R, L), dev, workspace, raw)
     st = native.dg_lora_bf16(p_x, ldx, p_a, p_b, p_ids, p_s, p_r, p_base, ld_base, p_out, ld_out, T, N,
                           K, R, L, p_ws, ws_bytes, raw)
     if st != 0:

@@ -60,3 +60,53 @@ def test_the_tensors_device_is_entered(call, current):
     with pytest.raises(Entered) as e:
         getattr(binding if hasattr(binding, call) else moe_ops, call)(*CALLS[call])
     assert e.value.args == (1,)
+
+
+class Allocated(Exception):
+    pass
+
+
+@pytest.mark.parametrize("call", list(CALLS))
+def test_outputs_belong_to_the_stream_that_is_given(call, monkeypatch):
+    """Outputs, and the zeros that the grouped calls' unwritten rows keep, are allocated with that
+    stream as the current one: nothing else orders them before the launch."""
+    entered = []
+
+    class Stream:
+        device, cuda_stream = On.device, 0x1000
+
+    class Context:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            entered.append(self.stream)
+
+        def __exit__(self, *exc):
+            return False
+
+    def allocate(*args, **kwargs):
+        raise Allocated(tuple(entered))
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)
+    monkeypatch.setattr(torch.cuda, "stream", Context)
+    for name in ("empty", "zeros"):
+        monkeypatch.setattr(torch, name, allocate)
+    # the arguments' pointers are not looked at before the outputs are allocated
+    native = type("Native", (), {"rows": staticmethod(lambda *a: (0, 8)), "vector": staticmethod(lambda *a: 0)})
+    monkeypatch.setattr(moe_ops, "_native", native)
+    stream = Stream()
+    with pytest.raises(Allocated) as e:
+        getattr(binding if hasattr(binding, call) else moe_ops, call)(*CALLS[call], stream=stream)
+    assert e.value.args == ((stream,),)
+
+
+@pytest.mark.parametrize("call", list(CALLS))
+def test_a_stream_of_another_device_is_refused(call, monkeypatch):
+    class Stream:
+        device, cuda_stream = torch.device("cuda:0"), 0x1000
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)
+    monkeypatch.setattr(moe_ops, "_native", object())
+    with pytest.raises(ValueError, match="stream is on cuda:0"):
+        getattr(binding if hasattr(binding, call) else moe_ops, call)(*CALLS[call], stream=Stream())
