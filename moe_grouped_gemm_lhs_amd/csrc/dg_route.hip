@@ -588,8 +588,8 @@ __device__ __forceinline__ void tiny_row(const RouteArgs& a, int64_t row, int l,
       us = __builtin_fmaf(of_loss(e), s, us);
     }
     sum = group_sum<L>(sum);
-    n.inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    us = group_sum<L>(us) * n.inv;
+    n.inv = !a.coef || sum == 0.0f ? 0.0f : 1.0f / sum;
+    us = a.coef ? group_sum<L>(us) * n.inv : 0.0f;
   }
   // f(expert, its logit, its weight's gradient) for the row's choices
   auto each = [&](auto f) {
@@ -703,8 +703,9 @@ route_backward_kernel(RouteArgs a) {
       }
       sum = group_sum<L>(sum);
       tiny = live && a.coef && sum < kTinySum;
-      n.inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-      us = group_sum<L>(us) * n.inv;
+      // without the loss a NaN among the scores stays its own
+      n.inv = !a.coef || sum == 0.0f ? 0.0f : 1.0f / sum;
+      us = a.coef ? group_sum<L>(us) * n.inv : 0.0f;
     } else {
       n = softmax_row<L, V>(x, s);
 #pragma unroll

@@ -142,3 +142,25 @@ def test_rows_beside_tiny_ones_keep_their_bits(score, E, low):
         assert torch.equal(got[0::2], alone)
     for got, alone in zip(rows(mixed, gw), rows(z, gw[1::2].contiguous())):
         assert torch.equal(got[1::2], alone)
+
+
+@pytest.mark.parametrize("normalize", [False, True])
+def test_a_nan_stays_its_own_in_a_sigmoid_row_without_the_loss(normalize):
+    """Weights under sigmoid come from their own logits, and so do their gradients; the loss's
+    shares, and with them its gradient, meet the whole row."""
+    z = torch.randn(9, 40, device=DEV)
+    z[3, 7] = -math.inf                     # a score of 0, in no choice
+    ids, w, _, _, coef = dg.dg_moe_route(z, 4, score="sigmoid", normalize=normalize, balance=1.0)
+    gw = torch.randn(9, 4, device=DEV)
+    how = dict(score="sigmoid", normalize=normalize)
+    want = dg.dg_moe_route_backward(z, ids, grad_weights=gw, **how)
+    assert torch.isfinite(want).all()
+    z[3, 7] = math.nan
+    again = dg.dg_moe_route(z, 4, **how)
+    assert torch.equal(again[0], ids) and torch.equal(again[1], w)
+    got = dg.dg_moe_route_backward(z, ids, grad_weights=gw, **how)
+    others = torch.ones_like(z, dtype=torch.bool)
+    others[3, 7] = False
+    assert torch.equal(got[others], want[others])
+    got = dg.dg_moe_route_backward(z, ids, grad_weights=gw, coef=coef, **how)
+    assert torch.isnan(got[3]).all() and torch.isfinite(got[:3]).all() and torch.isfinite(got[4:]).all()
