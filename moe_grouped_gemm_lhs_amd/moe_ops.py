@@ -77,7 +77,7 @@ def _workspace(need, device, workspace, raw):
         if workspace.device != device or not workspace.is_contiguous():
             raise ValueError(f"workspace must be contiguous and on {device}")
         return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    key = (device.index, raw)
+    key = (device, raw)
     kept = _workspaces.get(key)
     capturing = torch.cuda.is_current_stream_capturing()
     if kept is not None and kept[2] >= need and not capturing:
@@ -92,19 +92,20 @@ def _workspace(need, device, workspace, raw):
     return kept
 
 
-def _score(score):
-    code = _SCORES.get(score)
-    if code is None:
-        raise ValueError(f"unknown score function {score!r} (softmax or sigmoid)")
-    return code
+def _unknown(score):
+    return ValueError(f"unknown score function {score!r} (softmax or sigmoid)")
 
 
 def _logits(logits):
-    if logits.dtype not in _IN_DTYPES:
-        raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
+    """Device, its index, dtype and the dtype's code."""
+    dtype = logits.dtype
+    code = _IN_DTYPES.get(dtype)
+    if code is None:
+        raise TypeError(f"logits must be float32 or bfloat16, got {dtype}")
     if logits.dim() != 2:
         raise ValueError("logits must be 2-D (T x E)")
-    return _device(logits, "logits")
+    dev = _device(logits, "logits")
+    return dev, dev.index, dtype, code
 
 
 # ------------------------------------------------------------------------------- gate
@@ -124,16 +125,18 @@ def dg_moe_route(logits, k, *, bias=None, row_valid=None, score="softmax", norma
     balance; loss and coef with a balance.  ids, weights, counts, loss, coef may be given
     to be written in place.  include/dg.h has the formulas."""
     native = _native or _load_native()
-    dev = _logits(logits)
-    if stream is not None or dev.index != torch._C._cuda_getDevice():
+    dev, index, dtype, code = _logits(logits)
+    if stream is not None or index != torch._C._cuda_getDevice():
         with binding._elsewhere(dev, stream):
             return dg_moe_route(logits, k, bias=bias, row_valid=row_valid, score=score,
                                 normalize=normalize, scale=scale, balance=balance, count=count,
                                 ids=ids, weights=weights, counts=counts, loss=loss, coef=coef,
                                 workspace=workspace)
     T, E = logits.shape
-    sc = _score(score)
-    p_logits, ld = native.rows(logits, "logits", logits.dtype, (T, E), dev)
+    sc = _SCORES.get(score)
+    if sc is None:
+        raise _unknown(score)
+    p_logits, ld = native.rows(logits, "logits", dtype, (T, E), dev)
     p_bias = native.vector(bias, "bias", torch.float32, (E,), dev)
     if row_valid is not None and row_valid.dtype is torch.bool:
         row_valid = row_valid.view(torch.uint8)
@@ -156,13 +159,13 @@ def dg_moe_route(logits, k, *, bias=None, row_valid=None, score="softmax", norma
     p_counts = native.vector(counts, "counts", torch.int32, (E,), dev)
     p_loss = native.vector(loss, "loss", torch.float32, (), dev)
     p_coef = native.vector(coef, "coef", torch.float32, (E,), dev)
-    raw = torch._C._cuda_getCurrentRawStream(dev.index)
+    raw = torch._C._cuda_getCurrentRawStream(index)
     ws, p_ws, ws_bytes = None, None, 0
     if counts is not None:
         ws, p_ws, ws_bytes = _workspace(native.dg_moe_route_workspace_bytes(T, E), dev, workspace, raw)
-    st = native.dg_moe_route(p_logits, _IN_DTYPES[logits.dtype], ld, p_bias, p_valid, T, E, k, sc,
-                          bool(normalize), scale, balance or 0.0, p_ids, p_weights, p_counts,
-                          p_loss, p_coef, p_ws, ws_bytes, raw)
+    st = native.dg_moe_route(p_logits, code, ld, p_bias, p_valid, T, E, k, sc, bool(normalize), scale,
+                             balance or 0.0, p_ids, p_weights, p_counts, p_loss, p_coef, p_ws,
+                             ws_bytes, raw)
     if st != 0:
         raise DGError(st, "dg_moe_route")
     return ids, weights, counts, loss, coef
@@ -176,8 +179,8 @@ def dg_moe_route_backward(logits, ids, *, grad_weights=None, coef=None, grad_los
     call, grad_loss a float32 scalar; None: 1).  ids, row_valid, score, normalize and scale
     as in the forward call."""
     native = _native or _load_native()
-    dev = _logits(logits)
-    if stream is not None or dev.index != torch._C._cuda_getDevice():
+    dev, index, dtype, code = _logits(logits)
+    if stream is not None or index != torch._C._cuda_getDevice():
         with binding._elsewhere(dev, stream):
             return dg_moe_route_backward(logits, ids, grad_weights=grad_weights, coef=coef,
                                          grad_loss=grad_loss, row_valid=row_valid, score=score,
@@ -186,8 +189,10 @@ def dg_moe_route_backward(logits, ids, *, grad_weights=None, coef=None, grad_los
     if ids.dim() != 2:
         raise ValueError("ids must be 2-D (T x k)")
     k = ids.shape[1]
-    sc = _score(score)
-    p_logits, ld = native.rows(logits, "logits", logits.dtype, (T, E), dev)
+    sc = _SCORES.get(score)
+    if sc is None:
+        raise _unknown(score)
+    p_logits, ld = native.rows(logits, "logits", dtype, (T, E), dev)
     if row_valid is not None and row_valid.dtype is torch.bool:
         row_valid = row_valid.view(torch.uint8)
     p_valid = native.vector(row_valid, "row_valid", torch.uint8, (T,), dev)
@@ -196,11 +201,11 @@ def dg_moe_route_backward(logits, ids, *, grad_weights=None, coef=None, grad_los
     p_coef = native.vector(coef, "coef", torch.float32, (E,), dev)
     p_gl = native.vector(grad_loss, "grad_loss", torch.float32, (), dev)
     if grad_logits is None:
-        grad_logits = torch.empty((T, E), dtype=logits.dtype, device=dev)
-    p_out, ld_out = native.rows(grad_logits, "grad_logits", logits.dtype, (T, E), dev)
+        grad_logits = torch.empty((T, E), dtype=dtype, device=dev)
+    p_out, ld_out = native.rows(grad_logits, "grad_logits", dtype, (T, E), dev)
     st = native.dg_moe_route_backward(
-        p_logits, _IN_DTYPES[logits.dtype], ld, p_valid, T, E, k, sc, bool(normalize), scale, p_ids,
-        p_gw, p_coef, p_gl, p_out, ld_out, torch._C._cuda_getCurrentRawStream(dev.index))
+        p_logits, code, ld, p_valid, T, E, k, sc, bool(normalize), scale, p_ids,
+        p_gw, p_coef, p_gl, p_out, ld_out, torch._C._cuda_getCurrentRawStream(index))
     if st != 0:
         raise DGError(st, "dg_moe_route_backward")
     return grad_logits
@@ -250,7 +255,8 @@ def dg_lora_bf16(X, A, B, ids, base=None, out=None, *, scales=None, ranks=None, 
     int32, None: all R.  base None: zero; out may be base itself.  Returns out."""
     native = _native or _load_native()
     dev = _device(X, "X")
-    if stream is not None or dev.index != torch._C._cuda_getDevice():
+    index = dev.index
+    if stream is not None or index != torch._C._cuda_getDevice():
         with binding._elsewhere(dev, stream):
             return dg_lora_bf16(X, A, B, ids, base, out, scales=scales, ranks=ranks,
                                 workspace=workspace)
@@ -270,7 +276,7 @@ def dg_lora_bf16(X, A, B, ids, base=None, out=None, *, scales=None, ranks=None, 
     if out is None:
         out = torch.empty((T, N), dtype=bf16, device=dev)
     p_out, ld_out = native.rows(out, "out", bf16, (T, N), dev)
-    raw = torch._C._cuda_getCurrentRawStream(dev.index)
+    raw = torch._C._cuda_getCurrentRawStream(index)
     ws, p_ws, ws_bytes = _workspace(native.dg_lora_workspace_bytes(T, N, K, R, L), dev, workspace, raw)
     st = native.dg_lora_bf16(p_x, ldx, p_a, p_b, p_ids, p_s, p_r, p_base, ld_base, p_out, ld_out, T, N,
                           K, R, L, p_ws, ws_bytes, raw)
