@@ -79,3 +79,26 @@ def test_threads_on_one_stream():
     for t in threads:
         t.join()
     assert not wrong, wrong
+
+
+@pytest.mark.parametrize("T,E", [(64, 256), (40, 128), (200, 40), (64, 257), (65, 256), (300, 256), (129, 8)])
+@pytest.mark.parametrize("k", [1, 3, 8, 16])
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_asking_for_counts_changes_no_bits(T, E, k, dtype, score):
+    """Calls with counts may take another shape (sigmoid: one workgroup and one launch, at and just
+    past the sizes where they do); choices and weights stay what they are."""
+    if k > E:
+        pytest.skip("more choices than experts")
+    g = torch.Generator(device=DEV)
+    g.manual_seed(T + E + k)
+    z = (2 * torch.randn(T, E, generator=g, device=DEV)).to(dtype)
+    z[T // 2] -= 95.0                          # tiny scores
+    bias = 0.1 * torch.randn(E, generator=g, device=DEV)
+    for normalize in (False, True):
+        for b in (None, bias):
+            how = dict(score=score, normalize=normalize, scale=2.5, bias=b)
+            ids, w, *_ = dg.dg_moe_route(z, k, **how)
+            ids2, w2, counts, *_ = dg.dg_moe_route(z, k, count=True, **how)
+            assert torch.equal(ids, ids2) and torch.equal(w, w2)
+            assert torch.equal(counts.long(), torch.bincount(ids[ids >= 0].long(), minlength=E))
