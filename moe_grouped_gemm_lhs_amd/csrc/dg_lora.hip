@@ -323,16 +323,26 @@ lora_down_rows_kernel(LoraArgs a) {
 // Many rows: an item is a run of rows of one adapter within a tile of 16 MT.  Every workgroup
 // counts the items for itself from the ids (64 rows a ballot), without a launch to plan it,
 // and then knows its share of them:
-//  - where dividing each item's K alike gives most workgroups one part (or each item as many
-//    as it may have), it takes that part;
-//  - otherwise the items' pieces of K, one item after the other, are dealt out evenly.  A
-//    piece is counted as its loads, RT for the adapter's ranks and one for each tile of 16
-//    that the run touches, so the single rows of a mixed batch and the ends of prompts
-//    within a tile cost what they cost.
+//  - each item's K is divided alike, into as many parts as give no workgroup two, and it takes
+//    its part or none;
+//  - or the items' pieces of K, one item after the other, are dealt out evenly.  A piece is
+//    counted as its loads, RT for the adapter's ranks and one for each tile of 16 that the run
+//    touches, so the single rows of a mixed batch and the ends of prompts within a tile cost
+//    what they cost.
+// Dealing uses every workgroup, but a share that begins within an item costs a second item's
+// start and sums.  It is done where it saves a workgroup kDealPays loads (and the items do not
+// have all their parts already).  Of 139 batches (T 130 to 8192, K 512 to 16384, all ranks) none
+// that saves 38 or less gained from it, but for one whose items are very uneven; of the 16 that
+// save 70 or more all but three did.  Divided alike and dealt, in us, by the loads saved:
+//     7  200 x 512 rank 8 mixed          15.4  19.5      71  8192 x 2048 rank 8, prompts    21.9  20.4
+//    12  256 x 7168 rank 32, prompts     23.6  30.3      88  4096 x 7168 rank 32, prompts   32.7  28.9
+//    20  3000 x 7168 rank 16, prompts    19.2  20.6     152  8192 x 4096 rank 8, prompts    29.9  24.1
+//    36  200 x 2048 rank 64 mixed        34.0  40.5     485  4096 x 7168 rank 128, prompts  80.9  63.5
 // An item's parts, at most a.S, are the workgroups that share it; their number goes to
 // `parts` for each of its rows.  8192 x 16384 of rank 64: 81 us, x alone at 3.3 TB/s (a sum over
 // 512 MB reads 3.9), A again from L2 for each row tile; 4096 x 2048 of rank 16: 9.4.
 constexpr int kCounts = 256;              // blocks of rows, at most
+constexpr float kDealPays = 64.0f;
 
 __device__ __forceinline__ int row_id(const LoraArgs& a, int64_t t) { return t < a.T ? a.ids[t] : -1; }
 
@@ -414,7 +424,9 @@ lora_down_kernel(LoraArgs a) {
   const uint32_t G = gridDim.x, pieces = a.K / 64, count = items[blocks];
   if (count == 0) return;
   const uint32_t alike = G / count < (uint32_t)a.S ? G / count : a.S;
-  const bool one = alike == (uint32_t)a.S || 10 * alike * count >= (pieces <= 24 * alike ? 7 : 9) * G;
+  // divided alike, a workgroup that has a part has every / busy loads; dealt, every / G
+  const float busy = (float)(alike * count), every = (float)loads[blocks] * (float)pieces;
+  const bool one = alike == (uint32_t)a.S || every * ((float)G - busy) < kDealPays * (float)G * busy;
   const uint32_t* first = one ? items : loads;
   const uint32_t span = one ? alike : pieces < 128 ? pieces : 128;
   const uint32_t all = first[blocks] * span;              // T <= kLoraRows: below 2^32
