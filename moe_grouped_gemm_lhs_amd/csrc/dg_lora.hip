@@ -751,9 +751,13 @@ void lora_plan(LoraArgs* a) {
   // 7168, 40 adapters of rank 64: 31.8 us, 32.5 with 64 columns a wave)
   const bool few = T <= kLoraFewRows;
   a->up_ct = few ? 2 : 4;
-  // an output that the caches would hardly hold is not kept in them: 8192 x 7168 (117 MB)
-  // 147.7 us instead of 155.5, 192.6 instead of 197.0 with a copy that reads it next; of 4096
-  // (59 MB) 38.1 instead of 43.8, but 63.5 and 63.2 with the copy
+  // Stores past the caches are faster by themselves at every size and slow whoever reads out
+  // next, which shows up to 56 MiB and not from 70 on (K = 512, rank 16; alone, and with a copy
+  // of out behind it, in us):
+  //    28 MiB (2048 x 7168)  25.0 -> 23.0  33.5 -> 34.4     98 (7168 x 7168)   68.6 -> 62.7  104.2 -> 103.5
+  //    56 (4096 x 7168)      39.4 -> 34.6  56.5 -> 58.3    112 (8192 x 7168)   63.5 -> 59.8  105.2 -> 106.0
+  //    70 (5120 x 7168)      52.9 -> 47.3  75.8 -> 74.6    168 (12288 x 7168)  92.8 -> 88.8  157.5 -> 156.2
+  //    84 (6144 x 7168)      58.7 -> 53.0  89.3 -> 85.7    224 (16384 x 7168) 114.6 -> 108.3 200.4 -> 198.5
   a->past_caches = T * a->N * 2 >= kLoraPastCaches;
   const int64_t up_tiles = cdiv(T, a->up_mt * kTile) * cdiv(a->N, kUpWaves * kTile * a->up_ct);
   // workgroups on the same rows: those that find nothing to do cost little beside few others

@@ -52,7 +52,7 @@ void launch_route_backward(const RouteArgs& a, hipStream_t stream);
 constexpr int kLoraMaxR = 128;
 constexpr int64_t kLoraFewRows = 128;
 constexpr int64_t kLoraRows = (int64_t)1 << 20;   // rows of a launch
-constexpr int64_t kLoraPastCaches = (int64_t)96 << 20;   // bytes of an output
+constexpr int64_t kLoraPastCaches = (int64_t)64 << 20;   // bytes of an output
 
 struct LoraArgs {
   const uint16_t* x;
