@@ -51,14 +51,14 @@ def build(verbose: bool = False) -> str:
 
 
 def build_marshal(verbose: bool = False) -> str:
-    """Host code only, against torch's headers and libdg.so."""
+    """Host code only, by the one compiler, against libdg.so and the headers of torch and Python."""
     import sysconfig
 
     import torch
     from torch.utils.cpp_extension import include_paths
 
     tmp = MARSHAL + f".tmp{os.getpid()}"
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+    cmd = [HIPCC, "-no-hip-rt", "-x", "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
            "-isystem", sysconfig.get_paths()["include"]]
     for path in include_paths():

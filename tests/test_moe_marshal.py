@@ -119,3 +119,16 @@ def test_calls_convert_their_arguments(native):
     assert native.dg_moe_route(None, *args[1:]) == 1
     with pytest.raises(OverflowError):
         native.dg_moe_route(args[0], 1 << 40, *args[2:])
+
+
+def test_one_compiler_builds_everything(monkeypatch):
+    """hipcc, or what HIPCC names, is all that a build calls."""
+    from moe_grouped_gemm_lhs_amd import build
+    commands = []
+    monkeypatch.setattr(build, "HIPCC", "/where/hipcc")
+    monkeypatch.setattr(build.subprocess, "check_call", lambda cmd, **kw: commands.append(cmd))
+    monkeypatch.setattr(build.os, "replace", lambda *a: None)
+    monkeypatch.setattr(build.os, "remove", lambda *a: None)
+    build.build()
+    assert len(commands) == len(build.SOURCES) + 2
+    assert all(c[0] == "/where/hipcc" for c in commands), [c[0] for c in commands]
