@@ -241,7 +241,10 @@ dg_status dg_transpose_fp8(const uint8_t *X, uint8_t *Y, int64_t rows, int64_t c
  *   weights  weights[t][j] = scale * s of the choice, divided, if `normalize` is non-zero,
  *            by the sum of the row's chosen scores.  The quotients keep their precision
  *            however small the scores are (sigmoid: down to about e^-600; scores below count
- *            as 0, and 0 / 0 as 0).  The bias is part of the choice only.
+ *            as 0, and 0 / 0 as 0).  The bias is part of the choice only.  It is added to the
+ *            logits: a correction that was trained to be added to the scores, as the gates
+ *            with one that keeps the experts balanced have it, orders experts differently,
+ *            and no bias on the logits does what it does.
  *   row_valid (T bytes or NULL: all rows): a row of 0 is padding.  Its logits may be
  *            anything; its ids are -1, its weights 0, and it is in no count, loss or gradient.
  * and over the rows:
@@ -251,8 +254,10 @@ dg_status dg_transpose_fp8(const uint8_t *X, uint8_t *Y, int64_t rows, int64_t c
  *            valid rows of p_te, with p = s (softmax) or s / sum_e s (sigmoid); 0 if V = 0.
  *            Its derivative by p_te, f being a constant, is the same for every valid row:
  *   coef     coef[e] = balance * f_e / V, what the backward pass needs of the loss.
- * A row of -inf only has no choice and no probabilities; a row with a NaN, or under softmax
- * with a +inf, has NaN weights and makes the loss NaN (ids stay in range).
+ * A row of -inf only has no choice and no probabilities.  Under softmax a row with a NaN or a
+ * +inf has NaN weights; under sigmoid the weights come from the choices' own logits and stay
+ * finite, so they do not show a NaN among the others.  A NaN, and under softmax a
+ * +inf, makes the loss NaN.  ids stay in range.
  *
  * 1 <= E <= 1024, 1 <= k <= min(E, 16), T >= 0 (T = 0: counts, loss and coef are written as
  * zeros, nothing else).  counts may be NULL; loss and coef are both given or both NULL, and
@@ -288,7 +293,8 @@ dg_status dg_moe_route(const void *logits, int dtype, int64_t ld, const float *b
  *   sum_tj grad_weights[t][j] weights[t][j] + grad_loss * loss
  * with the choice and the counts held constant.  logits, row_valid, score, normalize, scale
  * as in the forward call, ids and coef its outputs.  grad_weights NULL: no first term (ids
- * may then be NULL).  coef NULL: no second term; grad_loss (one fp32 in DEVICE memory) NULL
+ * may then be NULL).  coef NULL: no second term (a NaN of a sigmoid row then stays in its own
+ * element); grad_loss (one fp32 in DEVICE memory) NULL
  * with coef: 1.  ids outside [0, E) are skipped; a row's ids must differ from each other.
  * No workspace.  Errors and execution as above. */
 dg_status dg_moe_route_backward(const void *logits, int dtype, int64_t ld,

@@ -277,8 +277,8 @@ __device__ __forceinline__ bool seen_before(int id) {
 // Few rows: an item is the rows of one adapter in a tile of 16, whatever lies between them.
 // Every workgroup finds the items from the ids, and the workgroups are dealt out to them
 // evenly: S workgroups an item, a part of K each.  64 rows of 64 adapters of rank 16, K = 7168:
-// 5.9 us, of which four are the dependent trips to memory (ids, then x and A); 128 rows,
-// K = 1536, 8 adapters of ranks up to 64: 5.5.
+// 6.1 us, of which four are the dependent trips to memory (ids, then x and A); 128 rows,
+// K = 1536, 8 adapters of ranks up to 64: 6.4.
 template <int RT>
 __global__ void __launch_bounds__(64 * kDownWaves, 2)
 lora_down_rows_kernel(LoraArgs a) {
@@ -339,8 +339,8 @@ lora_down_rows_kernel(LoraArgs a) {
 //    20  3000 x 7168 rank 16, prompts    19.2  20.6     152  8192 x 4096 rank 8, prompts    29.9  24.1
 //    36  200 x 2048 rank 64 mixed        34.0  40.5     485  4096 x 7168 rank 128, prompts  80.9  63.5
 // An item's parts, at most a.S, are the workgroups that share it; their number goes to
-// `parts` for each of its rows.  8192 x 16384 of rank 64: 81 us, x alone at 3.3 TB/s (a sum over
-// 512 MB reads 3.9), A again from L2 for each row tile; 4096 x 2048 of rank 16: 9.4.
+// `parts` for each of its rows.  8192 x 16384 of rank 64: 82 us, x alone at 3.3 TB/s (a sum over
+// 512 MB reads 3.9), A again from L2 for each row tile; 4096 x 2048 of rank 16: 10.0.
 constexpr int kCounts = 256;              // blocks of rows, at most
 constexpr float kDealPays = 64.0f;
 
@@ -480,8 +480,8 @@ lora_down_kernel(LoraArgs a) {
 // TB/s here, by 128 at 3.95; 4096 x 7168).  h goes in as rounded + rest, RS 32-deep steps
 // each, from LDS, where the workgroup has put it for its rows; an adapter's weights are loaded
 // once for all its rows, those of NB adapters at a time.  Workgroup z = q takes the rows'
-// adapters of its q, and q = 0 the rows without one.  4096 x 7168 of rank 16: 30.7 us, base and
-// out at 3.8 TB/s; 128 x 24576 with 8 adapters of ranks up to 64: 14.2 us, 2.7 TB/s with B,
+// adapters of its q, and q = 0 the rows without one.  4096 x 7168 of rank 16: 32.6 us, base and
+// out at 3.6 TB/s; 128 x 24576 with 8 adapters of ranks up to 64: 15.8 us, 2.4 TB/s with B,
 // the adapters of a tile one pair after the other.
 template <int MT, int RS, int CT, int NB>
 __global__ void __launch_bounds__(64 * kUpWaves, RS <= 2 ? 3 : 2)

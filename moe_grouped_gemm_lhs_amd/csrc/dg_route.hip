@@ -158,7 +158,7 @@ __device__ __forceinline__ void order(double& a, double& b) {  // a >= b
   b = lo;
 }
 
-// Comparators of an odd-even merge sort of N = 2^n numbers.
+// Comparators of Batcher's odd-even merge sort of N = 2^n numbers.
 template <int N>
 struct SortNet {
   int n = 0;
@@ -295,9 +295,9 @@ __device__ __forceinline__ float coef_of(const RouteArgs& a, int n, int live) {
 }
 
 // A call of one workgroup ends with the sums over rows; the workgroups of a larger one leave
-// theirs to route_sums_kernel.  32768 x 256 fp32, 8 of each row, with the loss: 13.9 us (2.5
-// TB/s), then 5.6 for the sums; the networks' f64 instructions and their registers, which
-// leave two or three waves a SIMD to hide the loads, bound it.  64 x 256, one workgroup: 8.3.
+// theirs to route_sums_kernel.  32768 x 256 fp32, 8 of each row, with the loss: 15.7 us (2.2
+// TB/s), then 5.9 for the sums; the networks' f64 instructions and their registers, which
+// leave two or three waves a SIMD to hide the loads, bound it.  64 x 256, one workgroup: 8.5.
 template <int L, int V, int KM>
 __global__ void __launch_bounds__(kThreads, V == 32 ? 3 : 4)
 route_kernel(RouteArgs a) {
@@ -635,8 +635,9 @@ __device__ __forceinline__ void tiny_row(const RouteArgs& a, int64_t row, int l,
 // dz from the weights' gradients and the loss's (coef, the same for every row).  A row's
 // scores go through a row of LDS, where the lanes that keep its choices pick theirs up, and
 // the choices' score gradients through another, which is zero but for them.  A wave's next
-// rows are loaded before its present ones are worked on.  32768 x 256 fp32: 16.2 us, 4.2 TB/s
-// of 5.0 that a copy of 64 MB reaches; 8192 x 8 bf16: 3.8 us, a launch's latency.
+// rows are loaded before its present ones are worked on.  32768 x 256 fp32: 16.8 us, 4.1 TB/s
+// (a copy of 64 MB, as much as it reads and writes, reaches 5.0, one of 256 MB 5.4); 8192 x 8
+// bf16: 4.4 us, a launch's latency, 0.3 of it for the code of rows with tiny scores.
 template <int L, int V>
 __global__ void __launch_bounds__(kThreads)
 route_backward_kernel(RouteArgs a) {

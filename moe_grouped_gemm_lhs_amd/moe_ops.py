@@ -115,7 +115,8 @@ def dg_moe_route(logits, k, *, bias=None, row_valid=None, score="softmax", norma
     """The gate of a mixture of experts: the k experts of each row of logits (T x E, float32
     or bfloat16, rows may lie apart), their weights and what training needs.
 
-    bias (E float32) is added to the logits for the choice only (-inf closes an expert);
+    bias (E float32) is added to the logits, not to the scores, for the choice only (-inf
+    closes an expert);
     row_valid (T uint8 or bool) marks padding rows with 0; score is "softmax" or "sigmoid";
     normalize divides a row's weights by the sum of its chosen scores; scale multiplies
     them.  balance: the factor of the balance loss (None: no loss).
@@ -123,7 +124,10 @@ def dg_moe_route(logits, k, *, bias=None, row_valid=None, score="softmax", norma
     Returns (ids T x k int32, weights T x k float32, counts E int32 or None, loss float32
     scalar or None, coef E float32 or None): counts with count=True, a counts tensor or a
     balance; loss and coef with a balance.  ids, weights, counts, loss, coef may be given
-    to be written in place.  include/dg.h has the formulas."""
+    to be written in place.  include/dg.h has the formulas.
+
+    Nothing that is returned carries a gradient, also where logits does: moe_route is the
+    differentiable form."""
     native = _native or _load_native()
     dev, index, dtype, code = _logits(logits)
     if stream is not None or index != torch._C._cuda_getDevice():
@@ -252,7 +256,8 @@ def dg_lora_bf16(X, A, B, ids, base=None, out=None, *, scales=None, ranks=None, 
 
     X (T x K), base and out (T x N) are bfloat16 with rows that may lie apart; A (L x R x
     K) and B (L x N x R) bfloat16; ids (T) int32; scales (L) float32, None: 1; ranks (L)
-    int32, None: all R.  base None: zero; out may be base itself.  Returns out."""
+    int32, None: all R.  base None: zero; out may be base itself.  Returns out, which carries
+    no gradient whatever X, A, B or base do: there is no differentiable form."""
     native = _native or _load_native()
     dev = _device(X, "X")
     index = dev.index
