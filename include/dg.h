@@ -319,8 +319,9 @@ dg_status dg_moe_route_backward(const void *logits, int dtype, int64_t ld,
  *   stride, not overlap it otherwise)         out bf16, T x N, row stride ld_out
  * Rows of one adapter may be anywhere.  A row's result depends on its own adapter's values
  * only, whatever other adapters hold; an infinity or NaN in it makes the results that it
- * takes part in infinite or NaN.  Sums are fp32; the inner product is kept to 16
- * significant bits or more and the result rounded once, to nearest even.
+ * takes part in infinite or NaN.  Sums are fp32; the inner product (times the scale) is kept
+ * to 16 significant bits or more, as infinite past bf16's largest number, and the result
+ * rounded once, to nearest even.
  *
  * T, N >= 0 (0: nothing to do), K > 0 and K % 128 == 0, N, K <= 2^22, 8 <= R <= 128 and
  * R % 8 == 0, L >= 1, ldx % 8 == 0, strides at least the row's length (DG_ERR_SHAPE).

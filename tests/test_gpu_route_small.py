@@ -164,3 +164,46 @@ def test_a_nan_stays_its_own_in_a_sigmoid_row_without_the_loss(normalize):
     assert torch.equal(got[others], want[others])
     got = dg.dg_moe_route_backward(z, ids, grad_weights=gw, coef=coef, **how)
     assert torch.isnan(got[3]).all() and torch.isfinite(got[:3]).all() and torch.isfinite(got[4:]).all()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,E,k,ld,at", [(50, 20, 5, 31, 3), (9001, 24, 4, 24, 0), (2300, 1000, 6, 1003, 2),
+                                         (700, 8, 3, 9, 1)])
+def test_tiny_rows_among_others(score, dtype, T, E, k, ld, at):
+    """Every third row tiny, rows inside wider ones, padding, fewer open experts than choices, and
+    more rows than the grid takes at once; the gradient too goes into wider rows."""
+    rng = np.random.default_rng(T)
+    z = rng.standard_normal((T, E)).astype(np.float32)
+    bias = np.zeros(E, np.float32)
+    closed = rng.permutation(E)[: E - (k - 1)]            # k - 1 are open
+    bias[closed] = -math.inf
+    z[::3, np.setdiff1d(np.arange(E), closed)] -= 92.0
+    if score == "sigmoid":
+        z[::3] = z[::3].clip(max=-88.0)
+    valid = (rng.random(T) > 0.2).astype(np.uint8)
+    wide = torch.full((T, ld), float("nan"), dtype=dtype, device=DEV)
+    t = wide[:, at:at + E]
+    host = torch.from_numpy(z).to(dtype)
+    t.copy_(host)
+    t[torch.from_numpy(valid).to(DEV) == 0] = float("nan")
+    host = host.float().numpy()
+    ids, w, _, _, coef = check_forward(t, host, k, bias=bias, valid=valid, score=score, normalize=True,
+                                       scale=2.0)
+    assert (ids[:, k - 1] == -1).all()
+    gw = rng.standard_normal((T, k)).astype(np.float32)
+    out = torch.full((T, ld), 7.0, dtype=dtype, device=DEV)
+    dg.dg_moe_route_backward(t, ids, grad_weights=torch.from_numpy(gw).to(DEV), coef=coef, score=score,
+                             normalize=True, scale=2.0, row_valid=torch.from_numpy(valid).to(DEV),
+                             grad_logits=out[:, at:at + E])
+    some = np.unique(np.concatenate([np.arange(min(T, 60)), np.arange(T - 40, T)]))
+    want, size = R.route_grad(host[some], ids.cpu().numpy()[some], gw[some],
+                              coef.cpu().numpy().astype(np.float64), 1.0, valid[some], score, True, 2.0)
+    got = out[:, at:at + E].float().cpu().numpy()
+    tol = 3 * R.weight_tolerance(host, E) * size + (2.0 ** -8 * np.abs(want) if dtype == torch.bfloat16 else 0) \
+        + 1e-36
+    assert np.all(np.abs(got[some] - want) <= tol)
+    assert np.isfinite(got).all() and (got[valid == 0] == 0).all()
+    rest = torch.ones(ld, dtype=torch.bool, device=DEV)
+    rest[at:at + E] = False
+    assert (out[:, rest] == 7).all()
