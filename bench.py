@@ -578,6 +578,7 @@ def bench_quant(args, torch, np, dg, I, dev):
 
 _ROOT = os.path.dirname(os.path.abspath(__file__))
 _KERNEL_SOURCES = ["moe_grouped_gemm_lhs_amd/csrc/dg_kernels.hip",
+                   "moe_grouped_gemm_lhs_amd/csrc/dg_tile.h",
                    "moe_grouped_gemm_lhs_amd/csrc/dg_internal.h",
                    "moe_grouped_gemm_lhs_amd/csrc/dg_host.cpp"]
 _TRAFFIC_FILES = {

@@ -337,6 +337,127 @@ dg_status dg_lora_bf16(const uint16_t *X, int64_t ldx, const uint16_t *A, const 
                        int64_t T, int64_t N, int64_t K, int64_t R, int64_t L,
                        void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---------------------------------------------------------------------------------
+ * A feed-forward block in 8 bits, between and behind the GEMM calls: the norm in front, the
+ * gated first half, and the backward passes of both from 8-bit checkpoints.  Codes and
+ * scales are everywhere those of dg_quantize_fp8_1x128 (one fp32 scale per 128 columns of a
+ * row, amax / FMAX, 1 for a block of zeros; code = value / scale, nearest, ties to even),
+ * formed from fp32 values that are rounded nowhere before, so that they are the operands of
+ * the GEMM calls as they stand.  A block that holds a NaN has a NaN scale; one that holds an
+ * infinity (and no NaN) an infinite one.  All pointers are DEVICE pointers, T, rows and
+ * M_total may be 0 (nothing is done unless a call says otherwise), everything is
+ * asynchronous on `stream`, without readback, deterministic and graph-capturable, and no two
+ * buffers of a call may overlap unless a call says so.  Errors, in this order: DG_ERR_SHAPE,
+ * DG_ERR_FORMAT (formats, dtypes, activation), DG_ERR_NULL, DG_ERR_ALIGN, DG_ERR_WORKSPACE,
+ * DG_ERR_DEVICE, DG_ERR_HIP.
+ *
+ * Root-mean-square norm of T rows of K, behind the residual's addition:
+ *   h = X + residual   (fp32 sum rounded to `dtype`; residual NULL: h = X)
+ *   rstd = 1 / sqrt(mean of h^2 over the row + eps),   y = (h rstd) weight
+ * X, residual and H of `dtype` (DG_IN_F32 or DG_IN_BF16), weight K of weight_dtype (NULL: 1).
+ * Outputs, each NULL if it is not wanted: H (given if and only if residual is; it may be X or
+ * residual themselves, with the same stride), codes Q (T x K, dense) with scales S
+ * (T x K/128), Y = bf16(y) (its codes come from y, not from Y), rstd (T fp32, for the backward
+ * pass).  A row whose h^2 leave the fp32 range has rstd 0; one of zeros needs eps > 0; a row
+ * with a NaN is NaN.
+ * 0 < K <= 65536, K % 128 == 0; row strides at least K and multiples of 8 (DG_ERR_SHAPE).
+ * X, residual, weight, H, Y 16-byte aligned, Q 8, S and rstd 4. */
+dg_status dg_rms_norm_fp8(const void *X, int dtype, int64_t ldx, const void *residual,
+                          int64_t ld_residual, const void *weight, int weight_dtype, float eps,
+                          void *H, int64_t ldh, uint8_t *Q, float *S, int format, uint16_t *Y,
+                          int64_t ldy, float *rstd, int64_t T, int64_t K, void *stream);
+
+/* Backward pass of the norm, H and rstd being the forward call's (H = X without a residual):
+ *   g = weight grad_y,  grad_x = rstd (g - h rstd^2 mean(g h)) + grad_h
+ *   grad_weight = sum over rows of grad_y h rstd
+ * grad_x (dtype) is the gradient by X and by the residual alike; grad_h (dtype, NULL: none) is
+ * the gradient that reaches H itself, the residual stream's, and may be grad_x, as grad_y may
+ * (same stride).  grad_weight (K fp32, NULL: not wanted) is written, with zeros for T = 0; its
+ * sums are fp32, in an order that depends on the sizes only.  Shapes and alignments as above.
+ * With grad_weight a workspace of dg_rms_norm_backward_workspace_bytes bytes, 16-byte aligned,
+ * that may hold anything before and after (see dg_moe_route). */
+size_t dg_rms_norm_backward_workspace_bytes(int64_t T, int64_t K);
+dg_status dg_rms_norm_backward(const void *grad_y, int dtype, int64_t ld_grad_y, const void *H,
+                               int64_t ldh, const float *rstd, const void *weight,
+                               int weight_dtype, const void *grad_h, int64_t ld_grad_h,
+                               void *grad_x, int64_t ld_grad_x, float *grad_weight, int64_t T,
+                               int64_t K, void *workspace, size_t workspace_bytes,
+                               void *stream);
+
+/* The first half of a gated feed-forward block in one kernel:
+ *   G = A Bg^T,  U = A Bu^T   (block-scaled products as in dg_gemm_fp8_nt, kept in fp32)
+ *   h = act(G) U,   act(x) = x sigmoid(x)                                   (DG_ACT_SILU)
+ *                   act(x) = x sigmoid(2 sqrt(2/pi) (x + 0.044715 x^3))     (DG_ACT_GELU: the
+ *                                                                           tanh form of gelu)
+ * out as codes H (rows x N) and scales sH (rows x N/128) of out_format, the A operand of the
+ * down projection's call.  A, sA, B, sB, group_idx, masked_m, formats and row rules are those
+ * of the GEMM calls, with B (a group's) the gate's N rows and then the up matrix's N, sB their
+ * 2N/128 rows of scales.  GU and sGU (both or neither): codes (rows x 2N: gate, then up) and
+ * scales (rows x 2N/128) of G and U in out_format, the checkpoint for dg_gated_backward.  Rows
+ * that the GEMM call would not write keep what H, sH, GU and sGU held.
+ * N % 128 == 0, N <= 2^20, K % 128 == 0, 0 < K <= 2^22.  A, B, H, GU 16-byte aligned, the rest 4.
+ * Workspace: dg_gated_workspace_bytes(kind, rows or cap, N, K, G) bytes under the GEMM calls'
+ * rules (zero filled before first use and left so). */
+#define DG_ACT_SILU 0
+#define DG_ACT_GELU 1
+
+size_t dg_gated_workspace_bytes(int kind, int64_t rows_or_cap, int64_t N, int64_t K, int64_t G);
+dg_status dg_gated_fp8_nt(const uint8_t *A, int a_format, const float *sA, const uint8_t *B,
+                          int b_format, const float *sB, uint8_t *H, float *sH, int out_format,
+                          uint8_t *GU, float *sGU, int activation, int64_t M, int64_t N,
+                          int64_t K, void *workspace, size_t workspace_bytes, void *stream);
+dg_status dg_grouped_gated_fp8_contiguous(const uint8_t *A, int a_format, const float *sA,
+                                          const uint8_t *B, int b_format, const float *sB,
+                                          const int32_t *group_idx, uint8_t *H, float *sH,
+                                          int out_format, uint8_t *GU, float *sGU,
+                                          int activation, int64_t M_total, int64_t N, int64_t K,
+                                          int64_t G, void *workspace, size_t workspace_bytes,
+                                          void *stream);
+dg_status dg_grouped_gated_fp8_masked(const uint8_t *A, int a_format, const float *sA,
+                                      const uint8_t *B, int b_format, const float *sB,
+                                      const int32_t *masked_m, uint8_t *H, float *sH,
+                                      int out_format, int activation, int64_t G, int64_t cap,
+                                      int64_t N, int64_t K, void *workspace,
+                                      size_t workspace_bytes, void *stream);
+
+/* Backward pass of the gated half up to the gradients by G and U, from the checkpoint:
+ *   D = (grad_H u act'(g), grad_H act(g)),  g and u the values that GU and sGU stand for
+ * grad_H T x N of dtype (dense), GU and sGU as the forward call wrote them in gu_format; D
+ * (T x 2N: by the gate, then by up) and sD (T x 2N/128) in out_format: the A operand of the
+ * call that forms the gradient by A (with B transposed, dg_transpose_fp8) and P of the weight
+ * gradient.  D and sD may be GU and sGU.  group_idx (T, or NULL: every row) with G as in the
+ * contiguous call: rows that it would not write are neither read nor written.
+ * N % 128 == 0, N <= 2^20, T N <= 2^35.  grad_H 16-byte aligned, GU and D 8, the rest 4. */
+dg_status dg_gated_backward(const void *grad_H, int dtype, const uint8_t *GU, int gu_format,
+                            const float *sGU, const int32_t *group_idx, int activation,
+                            uint8_t *D, float *sD, int out_format, int64_t T, int64_t N,
+                            int64_t G, void *stream);
+
+/* A weight's gradient from two 8-bit matrices that lie row by row, such as a gradient's codes
+ * and an activation's checkpoint:
+ *   dW[n,k] = sum over rows t of  (sP[t,n/128] P[t,n]) (sQ[t,k/128] Q[t,k])
+ * P T x N, sP T x N/128, Q T x K, sQ T x K/128; dW N x K of dtype, added to if `accumulate` is
+ * non-zero, else overwritten.  In the grouped form dW is G x N x K and row t counts for group
+ * group_idx[t] by the contiguous call's rule; the others' codes and scales may be anything; a
+ * group without rows has a gradient of zeros (T = 0: zeros everywhere).
+ * The products' factors are bf16: a code is one, a code with its scales is rounded once to 8
+ * bits (exactly kept for scales that are powers of two); sums are fp32, in an order that
+ * depends on the sizes only.
+ * N, K % 128 == 0, N, K <= 2^22, G (N/128) (K/128) < 2^23.  P, Q, dW 16-byte aligned, the rest 4.
+ * Workspace: dg_wgrad_workspace_bytes bytes (G = 1 for the dense form), 16-byte aligned, that
+ * may hold anything before and after (see dg_moe_route). */
+size_t dg_wgrad_workspace_bytes(int64_t T, int64_t N, int64_t K, int64_t G);
+dg_status dg_wgrad_fp8(const uint8_t *P, int p_format, const float *sP, const uint8_t *Q,
+                       int q_format, const float *sQ, void *dW, int dtype, int accumulate,
+                       int64_t T, int64_t N, int64_t K, void *workspace,
+                       size_t workspace_bytes, void *stream);
+dg_status dg_grouped_wgrad_fp8_contiguous(const uint8_t *P, int p_format, const float *sP,
+                                          const uint8_t *Q, int q_format, const float *sQ,
+                                          const int32_t *group_idx, void *dW, int dtype,
+                                          int accumulate, int64_t M_total, int64_t N, int64_t K,
+                                          int64_t G, void *workspace, size_t workspace_bytes,
+                                          void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -8,6 +8,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,7 +19,8 @@ MARSHAL = os.path.join(PKG, "_marshal.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["dg_kernels.hip", "dg_quant.hip", "dg_noalloc.hip", "dg_route.hip", "dg_lora.hip",
-           "dg_host.cpp", "dg_ops_host.cpp"]
+           "dg_norm.hip", "dg_gated.hip", "dg_wgrad.hip", "dg_host.cpp", "dg_ops_host.cpp",
+           "dg_ffn_host.cpp"]
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
@@ -30,14 +32,13 @@ FLAGS = [
 
 def build(verbose: bool = False) -> str:
     """Compile every source and link libdg.so, then _marshal.so (always rebuilds)."""
-    objs = []
-    for src in SOURCES:
-        obj = os.path.join(CSRC, f"{src}.{os.getpid()}.o")
-        cmd = [HIPCC, *FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
-        if verbose:
+    objs = [os.path.join(CSRC, f"{src}.{os.getpid()}.o") for src in SOURCES]
+    cmds = [[HIPCC, *FLAGS, "-c", os.path.join(CSRC, src), "-o", obj] for src, obj in zip(SOURCES, objs)]
+    if verbose:
+        for cmd in cmds:
             print(" ".join(cmd), flush=True)
-        subprocess.check_call(cmd)
-        objs.append(obj)
+    with ThreadPoolExecutor(4) as pool:                # a compiler takes up to 2 GB
+        list(pool.map(lambda cmd: subprocess.check_call(cmd), cmds))
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp]
     if verbose:

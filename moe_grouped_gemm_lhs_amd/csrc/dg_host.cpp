@@ -247,6 +247,8 @@ dg_status run(int kind, int fa, int fb, GemmArgs& a, void* workspace, size_t wor
 
 }  // namespace
 
+int dg::current_gpu(int* num_cus) { return check_device(num_cus); }
+
 extern "C" {
 
 int dg_get_m_alignment_for_contiguous_layout(void) { return dg::kAlignM; }

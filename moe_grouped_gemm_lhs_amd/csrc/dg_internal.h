@@ -84,6 +84,10 @@ struct Instance {
 // Table of all instances compiled into the library (defined in dg_kernels.hip).
 const Instance* instances(int* count);
 
+// DG_OK if the current device is a gfx950 GPU, and its CUs, else DG_ERR_DEVICE (defined in
+// dg_host.cpp).
+int current_gpu(int* num_cus);
+
 // fp8 block quantisation launch (defined in dg_quant.hip); arguments already validated.
 void launch_quantize(int block128x128, int fmt, int bf16, const void* X, uint8_t* Q, float* S,
                      int64_t rows, int64_t K, int num_cus, hipStream_t stream);

@@ -1,8 +1,8 @@
-// dg_marshal.cpp -- the Python module _marshal: what the binding of the gate and the adapters
-// does for every argument of every call, in C++.  A decode step makes these calls once a layer
-// with a few microseconds of GPU work each; checking ten tensors through their Python
-// attributes and a ctypes call of twenty arguments took 7 us of the host's 12 (one token of
-// dg_lora_bf16, two launches).
+// dg_marshal.cpp -- the Python module _marshal: what the binding of the gate, the adapters
+// and the feed-forward operators does for every argument of every call, in C++.  A decode
+// step makes these calls once a layer with a few microseconds of GPU work each; checking ten
+// tensors through their Python attributes and a ctypes call of twenty arguments took 7 us of
+// the host's 12 (one token of dg_lora_bf16, two launches).
 //
 // vector() and rows() return at once for the usual argument; whatever else it may be goes to
 // the Python functions given to use_slow(), which find out what is wrong and say so.  The
@@ -142,6 +142,17 @@ PyMethodDef methods[] = {
     DG_METHOD("dg_moe_route_backward", Call<dg_moe_route_backward>::run),
     DG_METHOD("dg_lora_workspace_bytes", Call<dg_lora_workspace_bytes>::run),
     DG_METHOD("dg_lora_bf16", Call<dg_lora_bf16>::run),
+    DG_METHOD("dg_rms_norm_fp8", Call<dg_rms_norm_fp8>::run),
+    DG_METHOD("dg_rms_norm_backward_workspace_bytes", Call<dg_rms_norm_backward_workspace_bytes>::run),
+    DG_METHOD("dg_rms_norm_backward", Call<dg_rms_norm_backward>::run),
+    DG_METHOD("dg_gated_workspace_bytes", Call<dg_gated_workspace_bytes>::run),
+    DG_METHOD("dg_gated_fp8_nt", Call<dg_gated_fp8_nt>::run),
+    DG_METHOD("dg_grouped_gated_fp8_contiguous", Call<dg_grouped_gated_fp8_contiguous>::run),
+    DG_METHOD("dg_grouped_gated_fp8_masked", Call<dg_grouped_gated_fp8_masked>::run),
+    DG_METHOD("dg_gated_backward", Call<dg_gated_backward>::run),
+    DG_METHOD("dg_wgrad_workspace_bytes", Call<dg_wgrad_workspace_bytes>::run),
+    DG_METHOD("dg_wgrad_fp8", Call<dg_wgrad_fp8>::run),
+    DG_METHOD("dg_grouped_wgrad_fp8_contiguous", Call<dg_grouped_wgrad_fp8_contiguous>::run),
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods,

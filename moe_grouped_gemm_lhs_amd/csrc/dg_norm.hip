@@ -1,0 +1,283 @@
+// dg_norm.hip -- root-mean-square norm with the residual's addition in front and fp8 codes
+// with 1x128 scales behind, and its backward pass, for gfx950.
+//
+//   forward    h = x + r (rounded to x's type), rstd = 1 / sqrt(mean h^2 + eps),
+//              y = h rstd w; codes and scales of y as the quantisation's, bf16 y on request
+//   backward   g = w dy, dx = rstd (g - h rstd^2 mean(g h)) + grad_h, dw = sum_t dy h rstd
+//
+// Memory-bound: every value is loaded once, in 16-byte accesses, and stays in registers
+// between the row's sum and its use.  NW waves share a row and each lane holds C pieces of
+// 8 values, 64 NW 8 apart, so 16 lanes hold one 128-block.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "dg_block.h"
+#include "dg_ffn.h"
+
+namespace dg {
+namespace {
+
+// Eight weights from column c on: bf16, fp32 or ones.
+__device__ __forceinline__ void load_weight(const NormArgs& a, int c, float (&w)[8]) {
+  if (!a.w) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = 1.0f;
+  } else if (a.w_bf16) {
+    Eight<true> v;
+    v.load(a.w, c);
+    v.get(w);
+  } else {
+    Eight<false> v;
+    v.load(a.w, c);
+    v.get(w);
+  }
+}
+
+// Workgroups of max(NW, 4) waves: four rows for NW = 1, else one.
+template <bool BF16, int NW, int C>
+__global__ void __launch_bounds__(NW < 4 ? 256 : NW * 64)
+norm_kernel(NormArgs a) {
+  constexpr int ROWS = NW < 4 ? 4 / NW : 1;
+  static_assert(NW == 1 || NW >= 4, "one wave or whole workgroups a row");
+  __shared__ float part[NW < 4 ? 1 : NW];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t row = (int64_t)blockIdx.x * ROWS + (ROWS > 1 ? wave : 0);
+  if (row >= a.T) return;                      // a wave alone (NW = 1: no barrier below)
+  const int t = NW == 1 ? lane : (int)threadIdx.x;
+  Eight<BF16> v[C];
+  float sum = 0.0f;
+  {
+    Eight<BF16> r[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const int c = (i * NW * 64 + t) * 8;
+      v[i].zero();
+      r[i].zero();
+      if (c < a.K) {
+        v[i].load(a.x, row * a.ldx + c);
+        if (a.r) r[i].load(a.r, row * a.ldr + c);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      float x[8];
+      v[i].get(x);
+      if (a.r) {
+        float y[8];
+        r[i].get(y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] += y[e];
+        v[i].set(x);
+        v[i].get(x);
+        const int c = (i * NW * 64 + t) * 8;
+        if (c < a.K) v[i].store(a.h, row * a.ldh + c);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum = __builtin_fmaf(x[e], x[e], sum);
+    }
+  }
+  sum = wave_sum(sum);
+  if constexpr (NW > 1) {
+    if (lane == 0) part[wave] = sum;
+    __syncthreads();
+    sum = part[0];
+#pragma unroll
+    for (int i = 1; i < NW; ++i) sum += part[i];
+  }
+  const float rstd = 1.0f / sqrtf(sum / (float)a.K + a.eps);
+  if (a.rstd && t == 0) a.rstd[row] = rstd;
+  const int nkb = a.K / kBlockK;
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    const int c = (i * NW * 64 + t) * 8;
+    if (c >= a.K) continue;                    // whole groups of 16 lanes: K is 128 n
+    float x[8], w[8];
+    v[i].get(x);
+    load_weight(a, c, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = x[e] * rstd * w[e];
+    if (a.y) {
+      Eight<true> y;
+      y.set(x);
+      y.store(a.y, row * a.ldy + c);
+    }
+    if (a.q) {
+      const float scale = block_scale(block_amax(x), a.fmt);
+      *(uint2*)(a.q + row * a.K + c) = codes8(x, scale, a.fmt);
+      if ((lane & 15) == 0) a.s[row * nkb + c / kBlockK] = scale;
+    }
+  }
+}
+
+// Backward: a workgroup takes rows blockIdx, blockIdx + gridDim, ... and keeps its columns'
+// sums of dy h rstd in registers.
+template <bool BF16, int NW, int C>
+__global__ void __launch_bounds__(NW * 64)
+norm_backward_kernel(NormArgs a) {
+  __shared__ float part[2][NW];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, t = threadIdx.x;
+  float dw[C][8];
+#pragma unroll
+  for (int i = 0; i < C; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dw[i][e] = 0.0f;
+  int flip = 0;
+  for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x, flip ^= 1) {
+    const float rstd = a.rstd[row];
+    Eight<BF16> vy[C], vh[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const int c = (i * NW * 64 + t) * 8;
+      vy[i].zero();
+      vh[i].zero();
+      if (c < a.K) {
+        vy[i].load(a.x, row * a.ldx + c);
+        vh[i].load(a.r, row * a.ldr + c);
+      }
+    }
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const int c = (i * NW * 64 + t) * 8;
+      float y[8], h[8], w[8];
+      vy[i].get(y);
+      vh[i].get(h);
+      if (c < a.K) load_weight(a, c, w);
+      else
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float p = y[e] * h[e];
+        dw[i][e] = __builtin_fmaf(p, rstd, dw[i][e]);
+        sum = __builtin_fmaf(p, w[e], sum);
+      }
+    }
+    sum = wave_sum(sum);
+    if (lane == 0) part[flip][wave] = sum;
+    __syncthreads();
+    sum = part[flip][0];
+#pragma unroll
+    for (int i = 1; i < NW; ++i) sum += part[flip][i];
+    const float m = sum / (float)a.K * rstd * rstd;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const int c = (i * NW * 64 + t) * 8;
+      if (c >= a.K) continue;
+      float y[8], h[8], w[8];
+      vy[i].get(y);
+      vh[i].get(h);
+      load_weight(a, c, w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = rstd * (y[e] * w[e] - h[e] * m);
+      Eight<BF16> o;
+      if (a.grad_h) {
+        float g[8];
+        o.load(a.grad_h, row * a.ld_gh + c);
+        o.get(g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] += g[e];
+      }
+      o.set(y);
+      o.store(a.h, row * a.ldh + c);
+    }
+  }
+  if (!a.grad_w) return;
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    const int c = (i * NW * 64 + t) * 8;
+    if (c >= a.K) continue;
+    Eight<false> o;
+    o.set(dw[i]);
+    o.store(a.partial, (int64_t)blockIdx.x * a.K + c);
+  }
+}
+
+// The workgroups' sums added up: 64 columns a workgroup, 16 waves over its rows.
+__global__ void __launch_bounds__(1024) norm_weight_kernel(const float* partial, float* grad_w, int K, int n) {
+  __shared__ float part[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c = blockIdx.x * 64 + lane;        // K is a multiple of 64
+  float sum = 0.0f;
+  for (int i = wave; i < n; i += 16) sum += partial[(int64_t)i * K + c];
+  part[wave][lane] = sum;
+  __syncthreads();
+  if (wave == 0) {
+#pragma unroll
+    for (int i = 1; i < 16; ++i) sum += part[i][lane];
+    grad_w[c] = sum;
+  }
+}
+
+template <bool BF16, int NW, int C>
+void launch_forward(const NormArgs& a, hipStream_t stream) {
+  constexpr int rows = NW < 4 ? 4 / NW : 1;
+  hipLaunchKernelGGL((norm_kernel<BF16, NW, C>), dim3((unsigned)((a.T + rows - 1) / rows)),
+                     dim3(NW < 4 ? 256 : NW * 64), 0, stream, a);
+}
+
+template <bool BF16>
+void forward_for(const NormArgs& a, hipStream_t stream) {
+  const int pieces = (a.K + 511) / 512;        // of 512 values, a wave's worth
+  if (pieces <= 1) return launch_forward<BF16, 1, 1>(a, stream);
+  if (pieces <= 4) return launch_forward<BF16, 4, 1>(a, stream);
+  if (pieces <= 8) return launch_forward<BF16, 4, 2>(a, stream);
+  if (pieces <= 16) return launch_forward<BF16, 4, 4>(a, stream);
+  if (pieces <= 32) return launch_forward<BF16, 16, 2>(a, stream);
+  if (pieces <= 64) return launch_forward<BF16, 16, 4>(a, stream);
+  return launch_forward<BF16, 16, 8>(a, stream);
+}
+
+template <bool BF16, int NW, int C>
+void launch_back(const NormArgs& a, int grid, hipStream_t stream) {
+  hipLaunchKernelGGL((norm_backward_kernel<BF16, NW, C>), dim3(grid), dim3(NW * 64), 0, stream, a);
+}
+
+template <bool BF16>
+void backward_for(const NormArgs& a, int grid, hipStream_t stream) {
+  const int pieces = (a.K + 511) / 512;
+  if (pieces <= 4) return launch_back<BF16, 4, 1>(a, grid, stream);
+  if (pieces <= 8) return launch_back<BF16, 4, 2>(a, grid, stream);
+  if (pieces <= 16) return launch_back<BF16, 4, 4>(a, grid, stream);
+  if (pieces <= 32) return launch_back<BF16, 16, 2>(a, grid, stream);
+  if (pieces <= 64) return launch_back<BF16, 16, 4>(a, grid, stream);
+  return launch_back<BF16, 16, 8>(a, grid, stream);
+}
+
+}  // namespace
+
+int norm_backward_grid(int64_t T, int64_t K) {
+  (void)K;
+  return (int)(T < kNormMaxGrid ? T : kNormMaxGrid);
+}
+
+// In slices of rows: a launch has less than 2^32 threads.
+void launch_norm(const NormArgs& args, hipStream_t stream) {
+  NormArgs a = args;
+  const int64_t e = a.bf16 ? 2 : 4;
+  for (int64_t left = args.T; left > 0; left -= a.T) {
+    a.T = left < kNormRows ? left : kNormRows;
+    a.bf16 ? forward_for<true>(a, stream) : forward_for<false>(a, stream);
+    a.x = (const uint8_t*)a.x + a.T * a.ldx * e;
+    if (a.r) {
+      a.r = (const uint8_t*)a.r + a.T * a.ldr * e;
+      a.h = (uint8_t*)a.h + a.T * a.ldh * e;
+    }
+    if (a.q) {
+      a.q += a.T * a.K;
+      a.s += a.T * (a.K / kBlockK);
+    }
+    if (a.y) a.y += a.T * a.ldy;
+    if (a.rstd) a.rstd += a.T;
+  }
+}
+
+void launch_norm_backward(const NormArgs& a, hipStream_t stream) {
+  const int grid = norm_backward_grid(a.T, a.K);
+  if (grid > 0) a.bf16 ? backward_for<true>(a, grid, stream) : backward_for<false>(a, grid, stream);
+  if (a.grad_w)
+    hipLaunchKernelGGL(norm_weight_kernel, dim3(a.K / 64), dim3(1024), 0, stream, a.partial, a.grad_w, a.K,
+                       grid);
+}
+
+}  // namespace dg

@@ -6,7 +6,14 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <mutex>
+
 namespace dg {
+
+// Held while the launches of a call that meet in its workspace are enqueued: of host threads
+// that share a workspace on a stream, one's launches are then never between another's.  Calls
+// with other workspaces go on meanwhile, but for one in 64.
+std::mutex& workspace_mutex(const void* workspace);
 
 // First bytes of the gate's workspace, before its workgroups' sums.
 constexpr int kRouteWsHeader = 16;
