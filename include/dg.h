@@ -396,8 +396,8 @@ dg_status dg_rms_norm_backward(const void *grad_y, int dtype, int64_t ld_grad_y,
  * scales (rows x 2N/128) of G and U in out_format, the checkpoint for dg_gated_backward.  Rows
  * that the GEMM call would not write keep what H, sH, GU and sGU held.
  * N % 128 == 0, N <= 2^20, K % 128 == 0, 0 < K <= 2^22.  A, B, H, GU 16-byte aligned, the rest 4.
- * Workspace: dg_gated_workspace_bytes(kind, rows or cap, N, K, G) bytes under the GEMM calls'
- * rules (zero filled before first use and left so). */
+ * Workspace: dg_gated_workspace_bytes(kind, rows or cap, N, K, G) bytes (0 for many rows), 16-byte
+ * aligned, that may hold anything before and after (see dg_moe_route). */
 #define DG_ACT_SILU 0
 #define DG_ACT_GELU 1
 

@@ -49,9 +49,17 @@ struct GatedArgs : GemmArgs {  // N: rows of B, gate and up together
   uint8_t* GU;                 // codes of gate and up, rows x N, or nullptr
   float* sGU;
   int act, out_fmt;
+  float* scratch;              // few tiles: parts of sums, the workspace
 };
 
-void launch_gated(GatedArgs& a, int kind, int fmt_a, int fmt_b, int num_cus, hipStream_t stream);
+// What runs for these sizes (N: columns of H).
+struct GatedPlan {
+  int bm;                      // rows of a tile of the split kernels; 0: whole tiles
+  size_t bytes;                // of the workspace
+};
+GatedPlan gated_plan(int kind, int64_t rows, int64_t N, int64_t K, int64_t G);
+void launch_gated(GatedArgs& a, int kind, int fmt_a, int fmt_b, int num_cus, void* workspace,
+                  hipStream_t stream);
 
 struct GatedBackArgs {
   const void* dh;              // T x N

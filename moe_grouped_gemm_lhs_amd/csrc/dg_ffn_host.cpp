@@ -70,8 +70,10 @@ dg_status gated(int kind, const uint8_t* A, int a_format, const float* sA, const
   if (kind == dg::kMasked) a.masked_m = rows_of;
   a.H = H; a.sH = sH; a.GU = GU; a.sGU = sGU; a.act = activation; a.out_fmt = out_format;
   a.rows = (int)rows; a.N = (int)(2 * N); a.K = (int)K; a.G = (int)G;
+  std::unique_lock<std::mutex> together(dg::workspace_mutex(workspace), std::defer_lock);
+  if (need > 0) together.lock();
   (void)hipGetLastError();
-  dg::launch_gated(a, kind, a_format, b_format, num_cus, (hipStream_t)stream);
+  dg::launch_gated(a, kind, a_format, b_format, num_cus, workspace, (hipStream_t)stream);
   return launched();
 }
 
@@ -172,7 +174,8 @@ dg_status dg_rms_norm_backward(const void *grad_y, int dtype, int64_t ld_grad_y,
 size_t dg_gated_workspace_bytes(int kind, int64_t rows_or_cap, int64_t N, int64_t K, int64_t G) {
   if (kind < dg::kDense || kind > dg::kMasked || !gated_shape(kind, rows_or_cap, N, K, kind == dg::kDense ? 1 : G))
     return 0;
-  return 0;
+  if (rows_or_cap == 0 || N == 0) return 0;
+  return dg::gated_plan(kind, rows_or_cap, N, K, G).bytes;
 }
 
 dg_status dg_gated_fp8_nt(const uint8_t *A, int a_format, const float *sA, const uint8_t *B, int b_format,

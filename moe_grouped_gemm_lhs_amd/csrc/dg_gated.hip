@@ -47,12 +47,10 @@ __device__ __forceinline__ unsigned magnitude4(const v4f& v, unsigned m) {
   return m;
 }
 
-// The maximum over the lanes of a row: l16 of the four lane groups.
-__device__ __forceinline__ unsigned across_groups(unsigned m) {
-  const auto a = __builtin_amdgcn_permlane16_swap(m, m, false, false);
-  m = umax(a[0], a[1]);
-  const auto b = __builtin_amdgcn_permlane32_swap(m, m, false, false);
-  return umax(b[0], b[1]);
+// The maximum over the two lanes of a row.
+__device__ __forceinline__ unsigned across_halves(unsigned m) {
+  const auto a = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+  return umax(a[0], a[1]);
 }
 
 template <int FMT>
@@ -61,19 +59,18 @@ __device__ __forceinline__ unsigned codes4(const v4f& v, float scale, float r, b
   return tiny ? pack4<FMT, true>(x, scale, r) : pack4<FMT, false>(x, scale, r);
 }
 
-// Codes of a wave's 16 rows by 32 columns: lane (l16, q) has columns 16 j + 4 q .. + 3 of row
-// l16 in v[j]; a swap of lane groups gives it columns 16 (q & 1) + 8 (q >> 1) .. + 7, one 8-byte
-// store.
-typedef unsigned v2u __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ v2u codes_16x32(const v4f (&v)[2], float scale, int fmt) {
+// Codes of a wave's 32 rows by 32 columns: lane (l32, h) has columns 8 j + 4 h .. + 3 of row l32
+// in v[j]; swaps between the lane halves give it columns 16 h .. + 15, one 16-byte store.
+__device__ __forceinline__ v4i codes_32x32(const v4f (&v)[4], float scale, int fmt) {
   const float r = 1.0f / scale;
   const bool tiny = __builtin_amdgcn_ballot_w64(scale < kMinReciprocalScale) != 0;
-  unsigned c[2];
+  unsigned c[4];
 #pragma unroll
-  for (int j = 0; j < 2; ++j)
+  for (int j = 0; j < 4; ++j)
     c[j] = fmt == kFmtE5M2 ? codes4<kFmtE5M2>(v[j], scale, r, tiny) : codes4<kFmtE4M3>(v[j], scale, r, tiny);
-  const auto a = __builtin_amdgcn_permlane16_swap(c[0], c[1], false, false);
-  return (v2u){a[0], a[1]};
+  const auto a = __builtin_amdgcn_permlane32_swap(c[0], c[2], false, false);
+  const auto b = __builtin_amdgcn_permlane32_swap(c[1], c[3], false, false);
+  return (v4i){(int)a[0], (int)a[1], (int)b[0], (int)b[1]};
 }
 
 // Products of one staged K block.  The fp8 matrix instructions add 8 neighbouring products in
@@ -83,10 +80,15 @@ __device__ __forceinline__ v2u codes_16x32(const v4f (&v)[2], float scale, int f
 // (2^-27), at half the rate; the conversion is one instruction for two codes and runs beside the
 // matrix pipe.
 //
-// Per column fragment j: 16 MFMAs (four row fragments, four K quarters each, four chains side by
-// side), and between them the conversion of column fragment j + 1 and the promotion of j - 1.
+// v_mfma_f32_32x32x16_f16: lane (l32, h) supplies 8 codes of row l32 of each operand; which K
+// they are does not matter as long as both operands agree: the lane takes 16-byte chunks 2 u + h
+// of its row, two MFMAs each.  B is the first operand, so a lane's results are row l32 of A and
+// columns 8 e + 4 h .. + 3 of B, e = 0 .. 3: acc[2 I + e / 2][2 J + e % 2] of 32-row block I and
+// 32-column block J.
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef unsigned v4u __attribute__((ext_vector_type(4)));
 
 template <int FMT, bool HI>
 __device__ __forceinline__ unsigned to_f16(int w) {
@@ -94,74 +96,73 @@ __device__ __forceinline__ unsigned to_f16(int w) {
                                 : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((unsigned)w, 1.0f, HI);
   return __builtin_bit_cast(unsigned, v);
 }
-
-// The k-th pair of codes of a fragment (16 pairs) into its f16 form.
-struct HalfFrag {
-  unsigned w[16];
-  template <int FMT>
-  __device__ __forceinline__ void convert(const v8i& f, int k) {
-    w[k] = k & 1 ? to_f16<FMT, true>(f[k >> 1]) : to_f16<FMT, false>(f[k >> 1]);
-  }
-  __device__ __forceinline__ v8h quarter(int q) const {
-    typedef unsigned v4u __attribute__((ext_vector_type(4)));
-    const v4u v = {w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]};
-    return __builtin_bit_cast(v8h, v);
-  }
-};
+template <int FMT>
+__device__ __forceinline__ v8h to_f16x8(int lo, int hi) {
+  const v4u v = {to_f16<FMT, false>(lo), to_f16<FMT, true>(lo), to_f16<FMT, false>(hi), to_f16<FMT, true>(hi)};
+  return __builtin_bit_cast(v8h, v);
+}
 
 template <class C>
 __device__ __forceinline__ void compute_stage_f16(const uint8_t* __restrict__ st, const TileCtx& c,
                                                   v4f (&acc)[C::TI][C::TJ]) {
-  constexpr int TI = C::TI, TJ = C::TJ, WM = C::WM, WN = C::WN;
-  static_assert(TI == 4, "16 MFMAs, conversions and promotions a column fragment");
-  const uint8_t* As = st;
-  const uint8_t* Bs = st + C::A_BYTES;
+  constexpr int NI = C::WM / 32, NJ = C::WN / 32, NF = NI + NJ;
   const float* Ss = (const float*)(st + C::A_BYTES + C::B_BYTES);
-  const int q = c.q, l16 = c.l16;
-  const int lo = l16 * kBlockK + ((q ^ (l16 & 7)) << 4);
-  const int hi = l16 * kBlockK + (((q + 4) ^ (l16 & 7)) << 4);
-  const uint8_t* a_lo = As + c.wm * WM * kBlockK + lo;
-  const uint8_t* a_hi = As + c.wm * WM * kBlockK + hi;
-  const uint8_t* b_lo = Bs + c.wn * WN * kBlockK + lo;
-  const uint8_t* b_hi = Bs + c.wn * WN * kBlockK + hi;
-  HalfFrag af[TI], bf[2];
-  v8i raw = read_frag_block(b_lo, b_hi, 0);
+  const int l32 = c.lane & 31, h = c.lane >> 5;
+  const uint8_t* as = st + (c.wm * C::WM + l32) * kBlockK;
+  const uint8_t* bs = st + C::A_BYTES + (c.wn * C::WN + l32) * kBlockK;
+  // operands 0 .. NI - 1: rows of A, then columns of B; chunk 2 u + h at its swizzled slot
+  auto read = [&](int f, int u) {
+    const int slot = ((2 * u + h) ^ (l32 & 7)) << 4;
+    return f < NI ? *(const v4i*)(as + f * 32 * kBlockK + slot) : *(const v4i*)(bs + (f - NI) * 32 * kBlockK + slot);
+  };
+  auto convert = [&](int f, const v4i& w, int half) {
+    return f < NI ? to_f16x8<C::FMT_A>(w[2 * half], w[2 * half + 1]) : to_f16x8<C::FMT_B>(w[2 * half], w[2 * half + 1]);
+  };
+  v4i raw[2][NF];
+  v8h op[2][NF];
 #pragma unroll
-  for (int k = 0; k < 16; ++k) bf[0].template convert<C::FMT_B>(raw, k);
-  raw = read_frag_block(b_lo, b_hi, 1);
-  float sg[TI], su[TI];
+  for (int f = 0; f < NF; ++f) raw[0][f] = read(f, 0);
   const float s0 = Ss[C::BM], s1 = Ss[C::BM + 1];
+  float sa[NI];
 #pragma unroll
-  for (int i = 0; i < TI; ++i) {
-    const v8i f = read_frag_block(a_lo, a_hi, i);
+  for (int i = 0; i < NI; ++i) sa[i] = Ss[c.wm * C::WM + 32 * i + l32];
 #pragma unroll
-    for (int k = 0; k < 16; ++k) af[i].template convert<C::FMT_A>(f, k);
-    const float sa = Ss[c.wm * WM + 16 * i + l16];
-    sg[i] = sa * s0;
-    su[i] = sa * s1;
-  }
+  for (int f = 0; f < NF; ++f) op[0][f] = convert(f, raw[0][f], 0);
+  v16f part[NI][NJ];
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) part[i][j][e] = 0.0f;
   __builtin_amdgcn_sched_barrier(0);
-  v4f part[2][TI];
 #pragma unroll
-  for (int j = 0; j <= TJ; ++j) {
+  for (int s = 0; s < 8; ++s) {                  // 16 deep each
+    if ((s & 1) == 0 && s < 6) {
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const int i = k & 3, kq = k >> 2;
-      if (j < TJ) {
-        const v4f zero = {0.f, 0.f, 0.f, 0.f};
-        part[j & 1][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-            bf[j & 1].quarter(kq), af[i].quarter(kq), kq == 0 ? zero : part[j & 1][i], 0, 0, 0);
-        if (j + 1 < TJ) bf[(j + 1) & 1].template convert<C::FMT_B>(raw, k);
+      for (int f = 0; f < NF; ++f) raw[((s >> 1) + 1) & 1][f] = read(f, (s >> 1) + 1);
+    }
+#pragma unroll
+    for (int k = 0; k < (NI * NJ > NF ? NI * NJ : NF); ++k) {
+      if (k < NI * NJ) {
+        const int i = k % NI, j = k / NI;
+        part[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(op[s & 1][NI + j], op[s & 1][i], part[i][j], 0, 0, 0);
       }
-      if (j > 0) {
-        const int u = k >> 2, e = k & 3;          // element e of row fragment u
-        const float sc = 2 * (j - 1) >= TJ ? su[u] : sg[u];
-        acc[u][j - 1][e] = __builtin_fmaf(part[(j - 1) & 1][u][e], sc, acc[u][j - 1][e]);
-      }
+      if (k < NF && s < 7) op[(s + 1) & 1][k] = convert(k, raw[((s + 1) >> 1) & 1][k], (s + 1) & 1);
       __builtin_amdgcn_sched_barrier(0);
     }
-    if (j + 2 < TJ) raw = read_frag_block(b_lo, b_hi, j + 2);
   }
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float sc = sa[i] * (2 * (32 * j + 8 * e) >= C::WN ? s1 : s0);
+        v4f& x = acc[2 * i + e / 2][2 * j + e % 2];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] = __builtin_fmaf(part[i][j][4 * e + k], sc, x[k]);
+      }
 }
 
 // The gated epilogue.  A 128-column block of a row lies in four waves (32 columns each): they
@@ -172,28 +173,31 @@ __device__ __forceinline__ void store_tile_gated(const v4f (&acc)[C::TI][C::TJ],
                                                  const TileOut& o, int wm, int wn, int lane,
                                                  const int32_t* gl, unsigned* red, bool computes) {
   static_assert(C::TJ == 4 && C::WAVES_N == 4, "32 gate and 32 up columns a wave");
+  constexpr int NI = C::WM / 32;
   int ln = lane;
   asm volatile("" : "+v"(ln));           // lane terms computed here, not kept live
-  const int l16 = ln & 15, q = ln >> 4;
+  const int l32 = ln & 31, half = ln >> 5;
   const bool save = p.GU != nullptr;
+  // columns 8 e + 4 half .. + 3 of 32-row block i: gate (k = 0) or up (1)
+  auto part = [&](int i, int k, int e) -> const v4f& { return acc[2 * i + e / 2][2 * k + e % 2]; };
   if (computes) {
 #pragma unroll
-    for (int i = 0; i < C::TI; ++i) {
+    for (int i = 0; i < NI; ++i) {
       unsigned mh = 0, mg = 0, mu = 0;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const v4f g = acc[i][j], u = acc[i][j + 2];
+      for (int e = 0; e < 4; ++e) {
+        const v4f g = part(i, 0, e), u = part(i, 1, e);
         mh = magnitude4(gated4(g, u, p.act), mh);
         mg = magnitude4(g, mg);
         mu = magnitude4(u, mu);
       }
-      mh = across_groups(mh);
-      const int r = 4 * (C::WM * wm + 16 * i + l16) + wn;
-      if (q == 0) red[r] = mh;
+      mh = across_halves(mh);
+      const int r = 4 * (C::WM * wm + 32 * i + l32) + wn;
+      if (half == 0) red[r] = mh;
       if (save) {
-        mg = across_groups(mg);
-        mu = across_groups(mu);
-        if (q == 0) {
+        mg = across_halves(mg);
+        mu = across_halves(mu);
+        if (half == 0) {
           red[4 * C::BM + r] = mg;
           red[8 * C::BM + r] = mu;
         }
@@ -215,28 +219,28 @@ __device__ __forceinline__ void store_tile_gated(const v4f (&acc)[C::TI][C::TJ],
     return __builtin_bit_cast(float, umax(umax(m[0], m[1]), umax(m[2], m[3])));
   };
 #pragma unroll
-  for (int i = 0; i < C::TI; ++i) {
-    const int r = C::WM * wm + 16 * i + l16;
+  for (int i = 0; i < NI; ++i) {
+    const int r = C::WM * wm + 32 * i + l32;
     bool row_ok = r < o.rows;
     if (KIND == kContiguous) row_ok = row_ok && o.lead0 == o.g && gl[r] == o.g;
-    const int col = col0 + 32 * wn + 16 * (q & 1) + 8 * (q >> 1);
-    const bool scale_ok = row_ok && q == 0 && wn == 0;
+    const int col = col0 + 32 * wn + 16 * half;
+    const bool scale_ok = row_ok && half == 0 && wn == 0;
     const unsigned* m = red + 4 * r;
-    v4f h[2];
+    v4f h[4];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) h[j] = gated4(acc[i][j], acc[i][j + 2], p.act);
+    for (int e = 0; e < 4; ++e) h[e] = gated4(part(i, 0, e), part(i, 1, e), p.act);
     const float sh = block_scale(block_max(m), p.out_fmt);
-    __builtin_amdgcn_raw_buffer_store_b64(codes_16x32(h, sh, p.out_fmt), rh, row_ok ? r * N + col : kPastTile,
-                                          0, 0);
+    __builtin_amdgcn_raw_buffer_store_b128(codes_32x32(h, sh, p.out_fmt), rh, row_ok ? r * N + col : kPastTile,
+                                           0, 0);
     __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(int, sh), rs,
                                           scale_ok ? (r * nb + col0 / kBlockK) * 4 : kPastTile, 0, 0);
     if (!save) continue;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {                    // gate, up
       const float s = block_scale(block_max(m + (4 + 4 * k) * C::BM), p.out_fmt);
-      const v4f v[2] = {acc[i][2 * k], acc[i][2 * k + 1]};
-      __builtin_amdgcn_raw_buffer_store_b64(codes_16x32(v, s, p.out_fmt), rg,
-                                            row_ok ? r * 2 * N + k * N + col : kPastTile, 0, 0);
+      const v4f v[4] = {part(i, k, 0), part(i, k, 1), part(i, k, 2), part(i, k, 3)};
+      __builtin_amdgcn_raw_buffer_store_b128(codes_32x32(v, s, p.out_fmt), rg,
+                                             row_ok ? r * 2 * N + k * N + col : kPastTile, 0, 0);
       __builtin_amdgcn_raw_buffer_store_b32(
           __builtin_bit_cast(int, s), rsg,
           scale_ok ? (r * 2 * nb + k * nb + col0 / kBlockK) * 4 : kPastTile, 0, 0);
@@ -245,10 +249,207 @@ __device__ __forceinline__ void store_tile_gated(const v4f (&acc)[C::TI][C::TJ],
   wait_vmcnt<0>();
 }
 
+// The split kernel's step: start the copy of a later block into `next`, then multiply the block
+// staged in `cur` (restrict-qualified: no read waits for the copy).
+template <class C>
+__device__ __forceinline__ void gated_step(uint8_t* __restrict__ next, const uint8_t* __restrict__ cur,
+                                           const TileCtx& cn, bool issue, int kb_next, const TileCtx& cc,
+                                           bool compute, v4f (&acc)[C::TI][C::TJ]) {
+  if (issue) issue_stage<C, true>(next, cn, kb_next);
+  if (compute) compute_stage_f16<C>(cur, cc, acc);
+}
+
+// ------------------------------------------------------------------------------------
+// Few tiles (decode, experts with few rows): the (tile, K block) iterations of the tiles that
+// have rows, tile after tile, are dealt out evenly to kSplitGrid workgroups, so that every CU
+// streams the same share of B.  There are no more tiles than workgroups, so a workgroup's range
+// lies in at most two tiles; it leaves the fp32 sums of each in a slot of its own in the
+// workspace, and a second kernel adds the slots of a tile in their order, forms h and quantises
+// it.  Nothing waits, and nothing in the workspace need be cleared.
+constexpr int kSplitGrid = 256;
+
+// Ranges that W iterations are dealt out to: of four at least (a range costs its first copies'
+// way to memory and the second kernel's reading of its slot), but no longer than a tile.
+__device__ __forceinline__ long split_ranges(long W, int nkb) {
+  const int least = nkb < 4 ? nkb : 4;
+  const long g = udiv(W, least);
+  return g < kSplitGrid ? g : kSplitGrid;
+}
+
+// The rows under masked_m (dense: all of one group) as the schedule sees them.
+template <class C>
+__device__ __forceinline__ MaskedPlan live_tiles(const GatedArgs& p, int lane) {
+  if (p.masked_m) return masked_plan<C>(p, lane);
+  MaskedPlan m;
+  m.mm = lane == 0 ? p.rows : 0;
+  m.rt = (m.mm + C::BM - 1) / C::BM;
+  m.incl = m.total = ((p.rows + C::BM - 1) / C::BM) * p.tiles_n;
+  return m;
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::NT)
+gated_split_kernel(GatedArgs p) {
+  constexpr int TI = C::TI, TJ = C::TJ, STAGES = C::STAGES;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[STAGES * C::STAGE_BYTES];
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  const int nkb = p.nkb;
+  const MaskedPlan mp = live_tiles<C>(p, lane);
+  const long W = (long)mp.total * nkb;
+  const long G = split_ranges(W, nkb);
+  const long g = blockIdx.x;
+  if (g >= G) return;
+  const long i_begin = stream_start<C>(g, W, G), i_end = stream_start<C>(g + 1, W, G);
+  const int t_first = (int)udiv(i_begin, nkb);
+
+  TileCtx cn;
+  cn.A = p.A;
+  cn.sA = p.sA;
+  cn.K = p.K;
+  cn.nkb = nkb;
+  cn.nnb = p.nnb;
+  cn.N = p.N;
+  cn.wave = wave;
+  cn.cw = wave - C::CW0;
+  cn.lane = lane;
+  cn.gslot = 0;
+  cn.wm = wave / C::WAVES_N;
+  cn.wn = wave - cn.wm * C::WAVES_N;
+  cn.q = lane >> 4;
+  cn.l16 = lane & 15;
+  TileCtx cc = cn;
+  v4f acc[TI][TJ];
+#pragma unroll
+  for (int i = 0; i < TI; ++i)
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) acc[i][j] = (v4f){0.f, 0.f, 0.f, 0.f};
+
+  // the copies run STAGES - 1 iterations ahead of the products, across the tiles' border
+  const int n_iter = (int)(i_end - i_begin);
+  int tc = t_first, kbn = (int)(i_begin - (long)t_first * nkb), kbc = kbn, sn = 0, sc = 0;
+  MaskedCursor mn = masked_seek<C>(mp, p.tiles_n, t_first), mc = mn;
+  auto at = [&](TileCtx& c, const MaskedCursor& m) {
+    masked_tile<C>(p, mp, m, c);
+    c.nb_first = c.n0 / (2 * kBlockK);
+  };
+  for (int step = 1 - STAGES; step < n_iter; ++step) {
+    if (step >= 0) {
+      wait_stage_copies<C, STAGES - 2>(wave, min(STAGES - 2, n_iter - 1 - step));
+      stage_barrier();
+    }
+    const bool issue = step + STAGES - 1 < n_iter;
+    at(cn, mn);
+    at(cc, mc);
+    gated_step<C>(smem + sn * C::STAGE_BYTES, smem + sc * C::STAGE_BYTES, cn, issue, kbn, cc, step >= 0, acc);
+    if (issue) {
+      sn = sn + 1 == STAGES ? 0 : sn + 1;
+      if (++kbn == nkb) {
+        kbn = 0;
+        if (step + STAGES < n_iter) masked_next<C>(mp, p.tiles_n, mn);
+      }
+    }
+    if (step < 0) continue;
+    sc = sc + 1 == STAGES ? 0 : sc + 1;
+    const bool tile_end = kbc == nkb - 1 || step == n_iter - 1;
+    if (++kbc == nkb) kbc = 0;
+    if (!tile_end) continue;
+    // the sums of this range's part of tile tc, row by row
+    float* slot = p.scratch + (size_t)(g * 2 + (tc != t_first)) * C::BM * C::BN;
+    const __amdgpu_buffer_rsrc_t rw = buffer_over(slot, C::BM * C::BN * 4);
+    const int l32 = lane & 31, half = lane >> 5;
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+      const int r = C::WM * cc.wm + 32 * (i / 2) + l32;
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) {                  // see compute_stage_f16
+        const int col = C::WN * cc.wn + 32 * (j / 2) + 8 * (2 * (i & 1) + (j & 1)) + 4 * half;
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i, acc[i][j]), rw,
+                                               r < cc.rows ? (r * C::BN + col) * 4 : kPastTile, 0, 0);
+        acc[i][j] = (v4f){0.f, 0.f, 0.f, 0.f};
+      }
+    }
+    ++tc;
+    if (step < n_iter - 1) masked_next<C>(mp, p.tiles_n, mc);
+  }
+}
+
+// A 128-column block of a row is 16 lanes' work, 8 columns each.
+template <class C>
+__global__ void __launch_bounds__(256)
+gated_finish_kernel(GatedArgs p) {
+  const int lane = threadIdx.x & 63, l = lane & 15;
+  const int nkb = p.nkb, N = p.N >> 1, nb = N / kBlockK;
+  const MaskedPlan mp = live_tiles<C>(p, lane);
+  const long W = (long)mp.total * nkb;
+  const long G = split_ranges(W, nkb);
+  // four blocks a wave, of one row tile or of neighbouring rows
+  const long b = ((long)blockIdx.x * 4 + (threadIdx.x >> 6)) * 4 + (lane >> 4);
+  const long row = udiv(b, nb);                       // of the capacity's
+  const int block = (int)(b - row * nb);
+  const int grp = p.masked_m ? (int)udiv(row, p.rows) : 0;
+  const int r = (int)(row - (long)grp * p.rows);
+  // every lane takes part in the shuffles, whether its row is one or not
+  const int lane_g = grp < 64 ? grp : 63;
+  const int mm = __shfl(mp.mm, lane_g, 64), incl = __shfl(mp.incl, lane_g, 64), rts = __shfl(mp.rt, lane_g, 64);
+  const bool live = grp < (p.masked_m ? p.G : 1) && r < mm;
+  float gate[8], up[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) gate[e] = up[e] = 0.0f;
+  if (live) {
+    const int col = block * kBlockK + 8 * l;           // of h
+    const int tn = col / (C::BN / 2), in = col % (C::BN / 2);
+    const long t = incl - (long)rts * p.tiles_n + (long)(r / C::BM) * p.tiles_n + tn;
+    const long x0 = t * nkb, x1 = x0 + nkb - 1;
+    const long gf = udiv((x0 + 1) * G + W - 1, W) - 1, gl = udiv((x1 + 1) * G + W - 1, W) - 1;
+    // only the first range can begin before the tile, which is then its second
+    const int first = stream_start<C>(gf, W, G) < x0;
+    const int n = (int)(gl - gf) + 1;
+    const float* s = p.scratch + (size_t)(gf * 2) * C::BM * C::BN + (size_t)(r % C::BM) * C::BN +
+                     in / C::GW * C::WN + in % C::GW;
+    constexpr size_t kSlot = (size_t)2 * C::BM * C::BN;
+    for (int k0 = 0; k0 < n; k0 += 4) {
+      v4f a[4][4];                                     // four ranges' loads in flight
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = min(k0 + k, n - 1);
+        const float* at = s + i * kSlot + (i == 0 && first ? kSlot / 2 : 0);
+        a[k][0] = *(const v4f*)at;
+        a[k][1] = *(const v4f*)(at + 4);
+        a[k][2] = *(const v4f*)(at + C::GW);
+        a[k][3] = *(const v4f*)(at + C::GW + 4);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (k0 + k >= n) break;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          gate[e] += a[k][e >> 2][e & 3];
+          up[e] += a[k][2 + (e >> 2)][e & 3];
+        }
+      }
+    }
+  }
+  float h[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) h[e] = gate[e] * act_sigmoid<false>(gate[e], p.act, nullptr) * up[e];
+  auto put = [&](const float (&x)[8], uint8_t* codes, float* scale) {
+    const float s = block_scale(block_amax(x), p.out_fmt);
+    const uint2 c = codes8(x, s, p.out_fmt);
+    if (!live) return;
+    *(uint2*)(codes + block * kBlockK + 8 * l) = c;
+    if (l == 0) scale[block] = s;
+  };
+  put(h, p.H + row * N, p.sH + row * nb);
+  if (!p.GU) return;
+  put(gate, p.GU + row * 2 * N, p.sGU + row * 2 * nb);
+  put(up, p.GU + row * 2 * N + N, p.sGU + row * 2 * nb + nb);
+}
+
 template <int FA, int FB> using Tile = GatedCfg<Cfg<128, 256, 2, 4, 3, false, FA, FB, 4>>;
+template <int FA, int FB> using Split64 = GatedCfg<Cfg<64, 128, 2, 4, 5, true, FA, FB>>;
 
 template <int KIND, class C>
-void launch(GatedArgs& a, int num_cus, hipStream_t stream) {
+void launch_tiles(GatedArgs& a, int num_cus, hipStream_t stream) {
   a.tiles_m = (a.rows + C::BM - 1) / C::BM;
   a.tiles_n = a.N / C::BN;
   a.num_tiles = a.tiles_m * a.tiles_n * (KIND == kMasked ? a.G : 1);
@@ -257,14 +458,25 @@ void launch(GatedArgs& a, int num_cus, hipStream_t stream) {
   hipLaunchKernelGGL((gemm_fp8_kernel<KIND, C, GatedArgs>), dim3(grid), dim3(C::NT), 0, stream, a);
 }
 
+// F: C for E4M3 operands, whose geometry is every format's.
+template <class C, class F>
+void launch_split(GatedArgs& a, int kind, hipStream_t stream) {
+  a.tiles_n = a.N / C::BN;
+  hipLaunchKernelGGL(gated_split_kernel<C>, dim3(kSplitGrid), dim3(C::NT), 0, stream, a);
+  const int64_t blocks = (int64_t)a.rows * (kind == kMasked ? a.G : 1) * (a.N / 2 / kBlockK);
+  hipLaunchKernelGGL(gated_finish_kernel<F>, dim3((unsigned)((blocks + 15) / 16)), dim3(256), 0, stream, a);
+}
+
 template <int FA, int FB>
-void launch_for(GatedArgs& a, int kind, int num_cus, hipStream_t stream) {
+void launch_for(GatedArgs& a, int kind, int num_cus, const GatedPlan& plan, hipStream_t stream) {
+  if (plan.bm == 64) return launch_split<Split64<FA, FB>, Split64<0, 0>>(a, kind, stream);
+  if (plan.bm == 128) return launch_split<Tile<FA, FB>, Tile<0, 0>>(a, kind, stream);
   if (kind == kDense)
-    launch<kDense, Tile<FA, FB>>(a, num_cus, stream);
+    launch_tiles<kDense, Tile<FA, FB>>(a, num_cus, stream);
   else if (kind == kContiguous)
-    launch<kContiguous, Tile<FA, FB>>(a, num_cus, stream);
+    launch_tiles<kContiguous, Tile<FA, FB>>(a, num_cus, stream);
   else
-    launch<kMasked, Tile<FA, FB>>(a, num_cus, stream);
+    launch_tiles<kMasked, Tile<FA, FB>>(a, num_cus, stream);
 }
 
 // ------------------------------------------------------------------------ backward pass
@@ -356,13 +568,41 @@ __global__ void __launch_bounds__(256) gated_backward_kernel(GatedBackArgs a) {
 
 }  // namespace
 
-void launch_gated(GatedArgs& a, int kind, int fmt_a, int fmt_b, int num_cus, hipStream_t stream) {
+// Whole tiles or split ones, by what either takes (microseconds, fitted to both sides measured
+// at 1 to 256 rows, dense, and 72 to 1024 rows of 1 to 8 groups).  Whole tiles: 1.55 for each K block,
+// in as many rounds as the tiles need; 64 rows of (2048, 7168) 84, of (16384, 512) 12.8.  Split: two
+// launches, the same work spread over the GPU (half of it in tiles of 64 rows) at 2.0 a block, and
+// the sums' way to memory and back: 64 rows of (2048, 7168) 21.5, of (16384, 512) 15.6; 128 rows
+// of (12288, 1536) 32 against 24.
+GatedPlan gated_plan(int kind, int64_t rows, int64_t N, int64_t K, int64_t G) {
+  GatedPlan p{};
+  if (kind == kContiguous || (kind == kMasked && G > 64)) return p;
+  const int64_t groups = kind == kMasked ? G : 1;
+  const int bm = rows <= 64 ? 64 : 128, cols = bm == 64 ? 64 : 128;
+  const int64_t tiles = (rows + bm - 1) / bm * groups * (N / cols);
+  if (tiles > kSplitGrid) return p;
+  const double nkb = (double)(K / kBlockK), t128 = (double)((rows + 127) / 128 * groups * (N / kBlockK));
+  const double whole = 3 + 1.55 * nkb;
+  const double sums = 2.0 * 8 * N * rows * groups * (kSplitGrid / t128 + 1);     // bytes, there and back
+  const double split = 11 + 2.0 * nkb * t128 / kSplitGrid * (bm == 64 ? 0.5 : 1) + sums / 5.4e6;
+  if (whole <= split) return p;
+  p.bm = bm;
+  p.bytes = (size_t)kSplitGrid * 2 * bm * (2 * cols) * 4;
+  return p;
+}
+
+void launch_gated(GatedArgs& a, int kind, int fmt_a, int fmt_b, int num_cus, void* workspace,
+                  hipStream_t stream) {
   a.nkb = a.K / kBlockK;
   a.nnb = a.N / kBlockK;
+  const GatedPlan plan = gated_plan(kind, a.rows, a.N / 2, a.K, a.G);
+  a.scratch = (float*)workspace;
   if (fmt_a == kFmtE4M3)
-    fmt_b == kFmtE4M3 ? launch_for<0, 0>(a, kind, num_cus, stream) : launch_for<0, 1>(a, kind, num_cus, stream);
+    fmt_b == kFmtE4M3 ? launch_for<0, 0>(a, kind, num_cus, plan, stream)
+                      : launch_for<0, 1>(a, kind, num_cus, plan, stream);
   else
-    fmt_b == kFmtE4M3 ? launch_for<1, 0>(a, kind, num_cus, stream) : launch_for<1, 1>(a, kind, num_cus, stream);
+    fmt_b == kFmtE4M3 ? launch_for<1, 0>(a, kind, num_cus, plan, stream)
+                      : launch_for<1, 1>(a, kind, num_cus, plan, stream);
 }
 
 void launch_gated_backward(const GatedBackArgs& a, int num_cus, hipStream_t stream) {

@@ -83,80 +83,6 @@ __device__ __forceinline__ void store_tile_bf16(const v4f (&acc)[C::TI][C::TJ], 
 // workgroup ever waits for another, so the result does not depend on which workgroups
 // run at the same time.  A workgroup holds at most two shared tiles: the first and the
 // last of its range.
-// Where the stream-K iterations of the masked form live.  Lane l of every wave holds
-// group l's row tiles under its masked_m (clamped to [0, cap]) and, scanned over the
-// lanes, the first tile of group l + 1 (the groups' tiles are row-major: all column tiles
-// of a group's first row tile, then its second row tile, ...).  At most 64 groups.
-struct MaskedPlan {
-  int mm;          // this lane's group: rows under masked_m
-  int rt;          // its row tiles
-  int incl;        // tiles of groups 0 .. lane
-  int total;       // tiles of all groups
-};
-
-template <class C>
-__device__ __forceinline__ MaskedPlan masked_plan(const GemmArgs& p, int lane) {
-  MaskedPlan m;
-  int v = lane < p.G ? p.masked_m[lane] : 0;
-  v = v < 0 ? 0 : (v > p.rows ? p.rows : v);
-  m.mm = v;
-  m.rt = (v + C::BM - 1) / C::BM;
-  int incl = m.rt * p.tiles_n;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const int u = __shfl_up(incl, off, 64);
-    if (lane >= off) incl += u;
-  }
-  m.incl = incl;
-  m.total = __builtin_amdgcn_readlane(incl, 63);
-  return m;
-}
-
-// A position in the masked form's tile sequence: group g, row tile r, column tile n.
-struct MaskedCursor {
-  int g, r, n;
-};
-
-// The cursor of tile t (t < total): its group is the number of groups whose tiles all
-// come before t.
-template <class C>
-__device__ __forceinline__ MaskedCursor masked_seek(const MaskedPlan& m, int tiles_n, int t) {
-  MaskedCursor c;
-  c.g = (int)__builtin_popcountll(__builtin_amdgcn_ballot_w64(m.incl <= t));
-  const int first = __builtin_amdgcn_readlane(m.incl, c.g) -
-                    __builtin_amdgcn_readlane(m.rt, c.g) * tiles_n;
-  const int o = t - first;
-  c.r = o / tiles_n;
-  c.n = o - c.r * tiles_n;
-  return c;
-}
-
-// The next tile after c (only called while there is one).
-template <class C>
-__device__ __forceinline__ void masked_next(const MaskedPlan& m, int tiles_n, MaskedCursor& c) {
-  if (++c.n < tiles_n) return;
-  c.n = 0;
-  if (++c.r < __builtin_amdgcn_readlane(m.rt, c.g)) return;
-  c.r = 0;
-  // the next group with at least one row tile
-  const uint64_t later = __builtin_amdgcn_ballot_w64(m.rt > 0) & ~((2ull << c.g) - 1);
-  c.g = later ? (int)__builtin_ctzll(later) : 64;
-}
-
-// Tile fields of the copy / math context for cursor c.
-template <class C>
-__device__ __forceinline__ void masked_tile(const GemmArgs& p, const MaskedPlan& m,
-                                            const MaskedCursor& c, TileCtx& x) {
-  const int g = c.g < 64 ? c.g : 0;
-  const int mm = __builtin_amdgcn_readlane(m.mm, g);
-  x.a_row0 = g * p.rows + c.r * C::BM;
-  x.rows = min(C::BM, mm - c.r * C::BM);
-  x.Bg = p.B + (size_t)g * p.N * p.K;
-  x.sBg = p.sB + (size_t)g * p.nnb * p.nkb;
-  x.n0 = c.n * C::BN;
-  x.nb_first = x.n0 / kBlockK;
-}
-
 // Reduction of a shared stream-K tile, spread over its contributors, none of which
 // depends on another making progress.  The tile's fragments are split into P parts
 // (fragment f of wave w is in part (w*TI*TJ + f) % P, P = min(reducers, fragments, 32),
@@ -289,17 +215,6 @@ __device__ __forceinline__ bool reduce_parts(int mask, int P, int n, int g_first
   }
   return true;
 }
-
-// n / d for n >= 0, d > 0: a 32-bit unsigned division when both fit (every realistic
-// launch: a 64-bit division is a long emulated sequence), else a 64-bit one.
-__device__ __forceinline__ long udiv(long n, long d) {
-  if ((unsigned long long)n <= 0xFFFFFFFFull && (unsigned long long)d <= 0xFFFFFFFFull)
-    return (long)((unsigned)n / (unsigned)d);
-  return (long)((unsigned long long)n / (unsigned long long)d);
-}
-
-template <class C>
-__device__ __forceinline__ long stream_start(long g, long W, long G) { return udiv(g * W, G); }
 
 template <int KIND, class C>
 __global__ void __launch_bounds__(C::NT)

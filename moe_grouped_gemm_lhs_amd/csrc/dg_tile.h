@@ -270,17 +270,18 @@ struct Cfg {
 };
 
 // The gated form: B's rows are a gate matrix and, behind it, an up matrix of the same N / 2
-// rows, and a tile of BN columns holds BN / 2 of each: the 64 columns of compute wave wn are
-// gate columns 32 wn .. + 31 of the tile's 128, and then the up columns of the same index, and
-// each of four copy waves brings the rows of one compute wave's columns.  After the stages and
-// the group indices, LDS holds for each row and wave column the largest |h|, |gate| and |up|.
+// rows, and a tile of BN columns holds BN / 2 of each: the WN columns of compute wave wn are GW =
+// WN / 2 gate columns from GW wn on and then the up columns of the same index.  A copy wave brings
+// the rows of one wave's columns, or those of their gate or up half.  After the stages and the
+// group indices, LDS holds for each row and wave column the largest |h|, |gate| and |up|.
 template <class Base>
 struct GatedCfg : Base {
   static constexpr bool GATED = true;
+  static constexpr int GW = Base::WN / 2;
   static constexpr int RED_OFF = Base::GI_OFF + 2 * Base::BM * 4;
   static constexpr int LDS_BYTES = RED_OFF + 3 * Base::BM * 4 * 4;
-  static_assert(Base::BN == 256 && Base::WAVES_N == 4 && Base::CW == 4 && Base::B_DMA == 8 &&
-                    Base::PFD == 0, "64 rows of B a copy wave, as many columns a compute wave");
+  static_assert(Base::WAVES_N == 4 && Base::PFD == 0, "four waves a row of the tile");
+  static_assert(Base::B_DMA * 8 == Base::WN || Base::B_DMA * 8 == GW, "rows of B a copy wave");
   static_assert(LDS_BYTES <= 160 * 1024, "LDS budget");
 };
 
@@ -420,16 +421,20 @@ __device__ __forceinline__ void issue_stage(uint8_t* __restrict__ st, const Tile
     for (int it = 0; it < C::A_DMA; ++it, ua += 8 * K)
       copy16s<0>(ra, lane_off, ua, st + da + it * 1024);
     if constexpr (C::GATED) {
-      // 32 rows of the gate matrix, then the same of the up matrix (N / 2 is a multiple of 128)
-      const int row0 = (c.n0 >> 1) + c.cw * 32;
-      const __amdgpu_buffer_rsrc_t rg = buffer_over(c.Bg + (size_t)row0 * K, 32 * K);
-      const __amdgpu_buffer_rsrc_t ru = buffer_over(c.Bg + (size_t)(row0 + (c.N >> 1)) * K, 32 * K);
+      // GW rows of the gate matrix and as many of the up matrix, or one of both (N / 2 is a
+      // multiple of 128)
+      constexpr bool BOTH = C::B_DMA * 8 == C::WN;
+      const int row0 = (c.n0 >> 1) + (BOTH ? c.cw : c.cw >> 1) * C::GW;
+      const int up0 = row0 + (c.N >> 1);
+      const __amdgpu_buffer_rsrc_t r0 =
+          buffer_over(c.Bg + (size_t)(!BOTH && (c.cw & 1) ? up0 : row0) * K, C::GW * K);
+      const __amdgpu_buffer_rsrc_t r1 = buffer_over(c.Bg + (size_t)up0 * K, C::GW * K);
       int u = kb * kBlockK;
       asm volatile("" : "+s"(u));
 #pragma unroll
-      for (int it = 0; it < 4; ++it, u += 8 * K) {
-        copy16s<0>(rg, lane_off, u, st + db + it * 1024);
-        copy16s<0>(ru, lane_off, u, st + db + (4 + it) * 1024);
+      for (int it = 0; it < C::GW / 8; ++it, u += 8 * K) {
+        copy16s<C::B_NT ? 2 : 0>(r0, lane_off, u, st + db + it * 1024);
+        if (BOTH) copy16s<C::B_NT ? 2 : 0>(r1, lane_off, u, st + db + (C::GW / 8 + it) * 1024);
       }
     } else {
 #pragma unroll
@@ -942,6 +947,92 @@ gemm_fp8_kernel(P p) {
   }
   tile_walk<KIND, C, false>(smem, smem, p, c, G, slot, nwork);
 }
+
+// ------------------------------------------------------------------------------------
+// Where the stream-K iterations of the masked form live.  Lane l of every wave holds
+// group l's row tiles under its masked_m (clamped to [0, cap]) and, scanned over the
+// lanes, the first tile of group l + 1 (the groups' tiles are row-major: all column tiles
+// of a group's first row tile, then its second row tile, ...).  At most 64 groups.
+struct MaskedPlan {
+  int mm;          // this lane's group: rows under masked_m
+  int rt;          // its row tiles
+  int incl;        // tiles of groups 0 .. lane
+  int total;       // tiles of all groups
+};
+
+template <class C>
+__device__ __forceinline__ MaskedPlan masked_plan(const GemmArgs& p, int lane) {
+  MaskedPlan m;
+  int v = lane < p.G ? p.masked_m[lane] : 0;
+  v = v < 0 ? 0 : (v > p.rows ? p.rows : v);
+  m.mm = v;
+  m.rt = (v + C::BM - 1) / C::BM;
+  int incl = m.rt * p.tiles_n;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int u = __shfl_up(incl, off, 64);
+    if (lane >= off) incl += u;
+  }
+  m.incl = incl;
+  m.total = __builtin_amdgcn_readlane(incl, 63);
+  return m;
+}
+
+// A position in the masked form's tile sequence: group g, row tile r, column tile n.
+struct MaskedCursor {
+  int g, r, n;
+};
+
+// The cursor of tile t (t < total): its group is the number of groups whose tiles all
+// come before t.
+template <class C>
+__device__ __forceinline__ MaskedCursor masked_seek(const MaskedPlan& m, int tiles_n, int t) {
+  MaskedCursor c;
+  c.g = (int)__builtin_popcountll(__builtin_amdgcn_ballot_w64(m.incl <= t));
+  const int first = __builtin_amdgcn_readlane(m.incl, c.g) -
+                    __builtin_amdgcn_readlane(m.rt, c.g) * tiles_n;
+  const int o = t - first;
+  c.r = o / tiles_n;
+  c.n = o - c.r * tiles_n;
+  return c;
+}
+
+// The next tile after c (only called while there is one).
+template <class C>
+__device__ __forceinline__ void masked_next(const MaskedPlan& m, int tiles_n, MaskedCursor& c) {
+  if (++c.n < tiles_n) return;
+  c.n = 0;
+  if (++c.r < __builtin_amdgcn_readlane(m.rt, c.g)) return;
+  c.r = 0;
+  // the next group with at least one row tile
+  const uint64_t later = __builtin_amdgcn_ballot_w64(m.rt > 0) & ~((2ull << c.g) - 1);
+  c.g = later ? (int)__builtin_ctzll(later) : 64;
+}
+
+// Tile fields of the copy / math context for cursor c.
+template <class C>
+__device__ __forceinline__ void masked_tile(const GemmArgs& p, const MaskedPlan& m,
+                                            const MaskedCursor& c, TileCtx& x) {
+  const int g = c.g < 64 ? c.g : 0;
+  const int mm = __builtin_amdgcn_readlane(m.mm, g);
+  x.a_row0 = g * p.rows + c.r * C::BM;
+  x.rows = min(C::BM, mm - c.r * C::BM);
+  x.Bg = p.B + (size_t)g * p.N * p.K;
+  x.sBg = p.sB + (size_t)g * p.nnb * p.nkb;
+  x.n0 = c.n * C::BN;
+  x.nb_first = x.n0 / kBlockK;
+}
+
+// n / d for n >= 0, d > 0: a 32-bit unsigned division when both fit (every realistic
+// launch: a 64-bit division is a long emulated sequence), else a 64-bit one.
+__device__ __forceinline__ long udiv(long n, long d) {
+  if ((unsigned long long)n <= 0xFFFFFFFFull && (unsigned long long)d <= 0xFFFFFFFFull)
+    return (long)((unsigned)n / (unsigned)d);
+  return (long)((unsigned long long)n / (unsigned long long)d);
+}
+
+template <class C>
+__device__ __forceinline__ long stream_start(long g, long W, long G) { return udiv(g * W, G); }
 
 }  // namespace
 }  // namespace dg

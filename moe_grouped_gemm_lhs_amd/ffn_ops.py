@@ -92,18 +92,6 @@ def _weight(native, weight, K, dev):
     return native.vector(weight, "weight", weight.dtype, (K,), dev), code
 
 
-def _zero_workspace(need, dev, workspace):
-    """The caller's workspace, or the one that the GEMM calls keep for this stream: zero filled,
-    and left so."""
-    if need == 0:
-        return None, None, 0
-    if workspace is None:
-        raise AssertionError("no call needs one")
-    if workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be contiguous and on {dev}")
-    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
-
-
 # ------------------------------------------------------------------------------- norm
 def dg_rms_norm_fp8(X, weight=None, *, residual=None, eps=1e-6, fmt="e4m3", codes=True, bf16=False,
                     save=False, Q=None, S=None, H=None, Y=None, rstd=None, stream=None):
@@ -248,7 +236,8 @@ def _gated(call, kind, A, sA, B, sB, rows_of, H, sH, activation, a_format, b_for
         p_gu = native.vector(GU, "GU", GU.dtype, (*lead, N2), dev)
         p_sgu = native.vector(sGU, "sGU", torch.float32, (*lead, N2 // 128), dev)
     raw = torch._C._cuda_getCurrentRawStream(dev.index)
-    ws, p_ws, ws_bytes = _zero_workspace(native.dg_gated_workspace_bytes(kind, rows, N, K, G), dev, workspace)
+    ws, p_ws, ws_bytes = moe_ops._workspace(native.dg_gated_workspace_bytes(kind, rows, N, K, G), dev, workspace,
+                                            raw)
     if kind == DG_DENSE:
         st = native.dg_gated_fp8_nt(p_a, fa, p_sa, p_b, fb, p_sb, p_h, p_sh, out, p_gu, p_sgu, act, rows, N, K,
                                     p_ws, ws_bytes, raw)
