@@ -86,9 +86,14 @@ struct WgradArgs {
   int64_t T;
   int N, K, G;
   int p_fmt, q_fmt, bf16, accumulate;
-  int splits;
+  int splits;                  // the plan's
+  bool big;
 };
-int wgrad_splits(int64_t T, int64_t N, int64_t K, int64_t G);
+struct WgradPlan {
+  bool big;                    // tiles of 256 x 256, else 128 x 128
+  int splits;                  // parts of the sum over rows
+};
+WgradPlan wgrad_plan(int64_t T, int64_t N, int64_t K, int64_t G);
 void launch_wgrad(const WgradArgs& a, hipStream_t stream);
 
 }  // namespace dg

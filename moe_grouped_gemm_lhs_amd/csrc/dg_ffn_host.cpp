@@ -98,7 +98,8 @@ dg_status wgrad(const uint8_t* P, int p_format, const float* sP, const uint8_t* 
   a.partial = (float*)workspace;
   a.T = T; a.N = (int)N; a.K = (int)K; a.G = (int)G;
   a.p_fmt = p_format; a.q_fmt = q_format; a.bf16 = dtype == DG_IN_BF16; a.accumulate = accumulate != 0;
-  a.splits = dg::wgrad_splits(T, N, K, G);
+  const dg::WgradPlan plan = dg::wgrad_plan(T, N, K, G);
+  a.splits = plan.splits; a.big = plan.big;
   std::unique_lock<std::mutex> together(dg::workspace_mutex(workspace), std::defer_lock);
   if (need > 0) together.lock();
   (void)hipGetLastError();
@@ -231,7 +232,7 @@ dg_status dg_gated_backward(const void *grad_H, int dtype, const uint8_t *GU, in
 
 size_t dg_wgrad_workspace_bytes(int64_t T, int64_t N, int64_t K, int64_t G) {
   if (!wgrad_shape(T, N, K, G)) return 0;
-  const int splits = dg::wgrad_splits(T, N, K, G);
+  const int splits = dg::wgrad_plan(T, N, K, G).splits;
   return splits > 1 ? (size_t)splits * G * N * K * 4 : 0;
 }
 
