@@ -341,9 +341,9 @@ dg_status dg_lora_bf16(const uint16_t *X, int64_t ldx, const uint16_t *A, const 
  * A feed-forward block in 8 bits, between and behind the GEMM calls: the norm in front, the
  * gated first half, and the backward passes of both from 8-bit checkpoints.  Codes and
  * scales are everywhere those of dg_quantize_fp8_1x128 (one fp32 scale per 128 columns of a
- * row, amax / FMAX, 1 for a block of zeros; code = value / scale, nearest, ties to even),
- * formed from fp32 values that are rounded nowhere before, so that they are the operands of
- * the GEMM calls as they stand.  A block that holds a NaN has a NaN scale; one that holds an
+ * row, amax / FMAX, 1 for a block of zeros; code = value / scale, nearest; a quotient within
+ * 2^-22 of itself of the border between two codes may go to either), formed from fp32 values
+ * that are rounded nowhere before: the operands of the GEMM calls as they stand.  A block that holds a NaN has a NaN scale; one that holds an
  * infinity (and no NaN) an infinite one.  All pointers are DEVICE pointers, T, rows and
  * M_total may be 0 (nothing is done unless a call says otherwise), everything is
  * asynchronous on `stream`, without readback, deterministic and graph-capturable, and no two
@@ -427,7 +427,7 @@ dg_status dg_grouped_gated_fp8_masked(const uint8_t *A, int a_format, const floa
  * call that forms the gradient by A (with B transposed, dg_transpose_fp8) and P of the weight
  * gradient.  D and sD may be GU and sGU.  group_idx (T, or NULL: every row) with G as in the
  * contiguous call: rows that it would not write are neither read nor written.
- * N % 128 == 0, N <= 2^20, T N <= 2^35.  grad_H 16-byte aligned, GU and D 8, the rest 4. */
+ * N % 128 == 0, N <= 2^20, T N <= 2^35.  grad_H, GU and D 16-byte aligned, the rest 4. */
 dg_status dg_gated_backward(const void *grad_H, int dtype, const uint8_t *GU, int gu_format,
                             const float *sGU, const int32_t *group_idx, int activation,
                             uint8_t *D, float *sD, int out_format, int64_t T, int64_t N,

@@ -53,15 +53,46 @@ __device__ __forceinline__ float block_amax(const float (&x)[8]) {
 __device__ __forceinline__ float block_scale(float amax, int fmt) {
   return amax == 0.0f ? 1.0f : amax / (fmt == kFmtE5M2 ? fp8_max<kFmtE5M2>() : fp8_max<kFmtE4M3>());
 }
-template <int FMT, bool TINY>
-__device__ __forceinline__ uint2 codes8_as(const float* x, float scale, float r) {
-  return make_uint2(pack4<FMT, TINY>(x, scale, r), pack4<FMT, TINY>(x + 4, scale, r));
+// Four codes by the scale's reciprocal (correctly rounded): the quotients are off by 1.5 units of
+// their last place at most, so the largest, FMAX, needs no clamp, and only a quotient that near
+// the border between two codes may go to the other one.  A third of the exact division's
+// instructions, which bound the kernels that use this.  Scales whose reciprocal may leave
+// fp32's range take the exact division (pack4).
+template <int FMT>
+__device__ __forceinline__ unsigned quick4(const float* x, float r) {
+  int v;
+  if (FMT == kFmtE5M2) {
+    v = __builtin_amdgcn_cvt_pk_bf8_f32(x[0] * r, x[1] * r, 0, false);
+    v = __builtin_amdgcn_cvt_pk_bf8_f32(x[2] * r, x[3] * r, v, true);
+  } else {
+    v = __builtin_amdgcn_cvt_pk_fp8_f32(x[0] * r, x[1] * r, 0, false);
+    v = __builtin_amdgcn_cvt_pk_fp8_f32(x[2] * r, x[3] * r, v, true);
+  }
+  return (unsigned)v;
+}
+// N codes (a multiple of four) of a lane in N / 4 words.
+template <int FMT, int N>
+__device__ __forceinline__ void codes_as(const float (&x)[N], float scale, unsigned (&c)[N / 4]) {
+  const float r = 1.0f / scale;
+  if (__builtin_amdgcn_ballot_w64(scale < kMinReciprocalScale) == 0) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) c[i] = quick4<FMT>(x + 4 * i, r);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) c[i] = pack4<FMT, true>(x + 4 * i, scale, r);
+  }
+}
+template <int N>
+__device__ __forceinline__ void codes(const float (&x)[N], float scale, int fmt, unsigned (&c)[N / 4]) {
+  if (fmt == kFmtE5M2)
+    codes_as<kFmtE5M2, N>(x, scale, c);
+  else
+    codes_as<kFmtE4M3, N>(x, scale, c);
 }
 __device__ __forceinline__ uint2 codes8(const float (&x)[8], float scale, int fmt) {
-  const float r = 1.0f / scale;
-  if (__builtin_amdgcn_ballot_w64(scale < kMinReciprocalScale) == 0)
-    return fmt == kFmtE5M2 ? codes8_as<kFmtE5M2, false>(x, scale, r) : codes8_as<kFmtE4M3, false>(x, scale, r);
-  return fmt == kFmtE5M2 ? codes8_as<kFmtE5M2, true>(x, scale, r) : codes8_as<kFmtE4M3, true>(x, scale, r);
+  unsigned c[2];
+  codes<8>(x, scale, fmt, c);
+  return make_uint2(c[0], c[1]);
 }
 
 // Eight consecutive bf16 or fp32 values as they lie in memory, and as fp32.

@@ -14,7 +14,7 @@ namespace dg {
 // Root-mean-square norm (defined in dg_norm.hip).
 constexpr int64_t kNormMaxK = 65536;
 constexpr int64_t kNormRows = (int64_t)1 << 20;   // rows of a launch
-constexpr int kNormMaxGrid = 1024;       // workgroups that keep sums of a weight's gradient
+constexpr int kNormMaxGrid = 512;       // workgroups that keep sums of a weight's gradient
 
 struct NormArgs {
   const void* x;               // T x K; backward: the gradient by y
@@ -35,8 +35,8 @@ struct NormArgs {
   float eps;
 };
 
-// Workgroups of the backward pass that keep a row of sums, for these sizes.
-int norm_backward_grid(int64_t T, int64_t K);
+// Workgroups of the backward pass, each of which keeps a row of sums.
+int norm_backward_grid(int64_t T);
 void launch_norm(const NormArgs& a, hipStream_t stream);
 void launch_norm_backward(const NormArgs& a, hipStream_t stream);
 
@@ -72,7 +72,7 @@ struct GatedBackArgs {
   int N, G;
   int bf16, act, gu_fmt, fmt;
 };
-void launch_gated_backward(const GatedBackArgs& a, int num_cus, hipStream_t stream);
+void launch_gated_backward(const GatedBackArgs& a, hipStream_t stream);
 
 // A weight's gradient (defined in dg_wgrad.hip).
 struct WgradArgs {

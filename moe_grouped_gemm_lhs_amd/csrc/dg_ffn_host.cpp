@@ -139,7 +139,7 @@ dg_status dg_rms_norm_fp8(const void *X, int dtype, int64_t ldx, const void *res
 
 size_t dg_rms_norm_backward_workspace_bytes(int64_t T, int64_t K) {
   if (!norm_shape(T, K)) return 0;
-  return (size_t)dg::norm_backward_grid(T, K) * (size_t)K * 4;
+  return (size_t)dg::norm_backward_grid(T) * (size_t)K * 4;
 }
 
 dg_status dg_rms_norm_backward(const void *grad_y, int dtype, int64_t ld_grad_y, const void *H, int64_t ldh,
@@ -216,7 +216,7 @@ dg_status dg_gated_backward(const void *grad_H, int dtype, const uint8_t *GU, in
     return DG_ERR_FORMAT;
   if (T == 0 || N == 0) return DG_OK;
   if (!grad_H || !GU || !sGU || !D || !sD) return DG_ERR_NULL;
-  if (!aligned(grad_H, 16) || !aligned(GU, 8) || !aligned(D, 8) || !aligned(sGU, 4) || !aligned(sD, 4) ||
+  if (!aligned(grad_H, 16) || !aligned(GU, 16) || !aligned(D, 16) || !aligned(sGU, 4) || !aligned(sD, 4) ||
       !aligned(group_idx, 4))
     return DG_ERR_ALIGN;
   int num_cus = 0;
@@ -226,7 +226,7 @@ dg_status dg_gated_backward(const void *grad_H, int dtype, const uint8_t *GU, in
   a.dh = grad_H; a.gu = GU; a.sgu = sGU; a.group_idx = group_idx; a.d = D; a.sd = sD; a.T = T; a.N = (int)N;
   a.G = (int)G; a.bf16 = dtype == DG_IN_BF16; a.act = activation; a.gu_fmt = gu_format; a.fmt = out_format;
   (void)hipGetLastError();
-  dg::launch_gated_backward(a, num_cus, (hipStream_t)stream);
+  dg::launch_gated_backward(a, (hipStream_t)stream);
   return launched();
 }
 

@@ -53,21 +53,16 @@ __device__ __forceinline__ unsigned across_halves(unsigned m) {
   return umax(a[0], a[1]);
 }
 
-template <int FMT>
-__device__ __forceinline__ unsigned codes4(const v4f& v, float scale, float r, bool tiny) {
-  const float x[4] = {v[0], v[1], v[2], v[3]};
-  return tiny ? pack4<FMT, true>(x, scale, r) : pack4<FMT, false>(x, scale, r);
-}
-
 // Codes of a wave's 32 rows by 32 columns: lane (l32, h) has columns 8 j + 4 h .. + 3 of row l32
 // in v[j]; swaps between the lane halves give it columns 16 h .. + 15, one 16-byte store.
 __device__ __forceinline__ v4i codes_32x32(const v4f (&v)[4], float scale, int fmt) {
-  const float r = 1.0f / scale;
-  const bool tiny = __builtin_amdgcn_ballot_w64(scale < kMinReciprocalScale) != 0;
-  unsigned c[4];
+  float x[16];
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    c[j] = fmt == kFmtE5M2 ? codes4<kFmtE5M2>(v[j], scale, r, tiny) : codes4<kFmtE4M3>(v[j], scale, r, tiny);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[4 * j + e] = v[j][e];
+  unsigned c[4];
+  codes<16>(x, scale, fmt, c);
   const auto a = __builtin_amdgcn_permlane32_swap(c[0], c[2], false, false);
   const auto b = __builtin_amdgcn_permlane32_swap(c[1], c[3], false, false);
   return (v4i){(int)a[0], (int)a[1], (int)b[0], (int)b[1]};
@@ -480,14 +475,15 @@ void launch_for(GatedArgs& a, int kind, int num_cus, const GatedPlan& plan, hipS
 }
 
 // ------------------------------------------------------------------------ backward pass
-// Eight codes as fp32 values.
-__device__ __forceinline__ void decode8(uint2 c, int fmt, float scale, float (&x)[8]) {
-  const unsigned w[2] = {c.x, c.y};
+// Sixteen codes as fp32 values.
+template <int FMT>
+__device__ __forceinline__ void decode16_as(uint4 c, float scale, float (&x)[16]) {
+  typedef float v2f __attribute__((ext_vector_type(2)));
+  const unsigned w[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    typedef float v2f __attribute__((ext_vector_type(2)));
+  for (int k = 0; k < 4; ++k) {
     v2f a, b;
-    if (fmt == kFmtE5M2) {
+    if (FMT == kFmtE5M2) {
       a = __builtin_amdgcn_cvt_pk_f32_bf8((int)w[k], false);
       b = __builtin_amdgcn_cvt_pk_f32_bf8((int)w[k], true);
     } else {
@@ -500,70 +496,89 @@ __device__ __forceinline__ void decode8(uint2 c, int fmt, float scale, float (&x
     x[4 * k + 3] = b[1] * scale;
   }
 }
+__device__ __forceinline__ void decode16(uint4 c, int fmt, float scale, float (&x)[16]) {
+  if (fmt == kFmtE5M2)
+    decode16_as<kFmtE5M2>(c, scale, x);
+  else
+    decode16_as<kFmtE4M3>(c, scale, x);
+}
 
-// dg = dh u act'(g), du = dh act(g), act' = s + g s (1 - s) dz/dg.  Memory-bound: 16 lanes
-// hold a 128-block, a wave four of them, U blocks of each lane group in flight.
-template <bool BF16>
+// Scale of a block in eight lanes with sixteen values each.
+__device__ __forceinline__ float scale16(const float (&x)[16], int fmt) {
+  unsigned m = magnitude(x[0]);
+#pragma unroll
+  for (int e = 1; e < 16; ++e) m = umax(m, magnitude(x[e]));
+  m = umax(m, dpp<kXor1>(m));
+  m = umax(m, dpp<kXor2>(m));
+  m = umax(m, dpp<kHalfMirror>(m));
+  return block_scale(__builtin_bit_cast(float, m), fmt);
+}
+
+// dg = dh u act'(g), du = dh act(g), act' = s + g s (1 - s) dz/dg.  Memory and the VALU bound it
+// alike (about 35 instructions an element, two of them quarter rate): 8 lanes hold a
+// 128-block, 16 elements each, so that codes too are loaded and stored 16 bytes a lane.
+template <bool BF16, int ACT>
 __global__ void __launch_bounds__(256) gated_backward_kernel(GatedBackArgs a) {
-  constexpr int U = 2;
-  const int lane = threadIdx.x & 63;
+  const int lane = threadIdx.x & 63, l = lane & 7;
   const int nb = a.N / kBlockK;
-  const int64_t blocks = a.T * nb;
-  const int64_t wave = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int l = lane & 15;
-  Eight<BF16> vh[U];
-  uint2 cg[U], cu[U];
-  float sg[U], su[U];
-  int64_t row[U];
-  int j[U];
-  bool live[U];
-#pragma unroll
-  for (int k = 0; k < U; ++k) {
-    const int64_t b = (wave * U + k) * 4 + (lane >> 4);
-    live[k] = b < blocks;
-    row[k] = live[k] ? b / nb : 0;
-    j[k] = live[k] ? (int)(b - row[k] * nb) : 0;
-    if (a.group_idx && live[k]) {
-      const int g = a.group_idx[row[k]];
-      live[k] = g >= 0 && g < a.G && g == a.group_idx[row[k] & ~(int64_t)(kAlignM - 1)];
-    }
-    vh[k].zero();
-    cg[k] = cu[k] = make_uint2(0, 0);
-    sg[k] = su[k] = 1.0f;
-    if (!live[k]) continue;
-    const int64_t at = row[k] * 2 * a.N + j[k] * kBlockK + 8 * l;
-    vh[k].load(a.dh, row[k] * a.N + j[k] * kBlockK + 8 * l);
-    cg[k] = *(const uint2*)(a.gu + at);
-    cu[k] = *(const uint2*)(a.gu + at + a.N);
-    sg[k] = a.sgu[row[k] * 2 * nb + j[k]];
-    su[k] = a.sgu[row[k] * 2 * nb + nb + j[k]];
+  const int64_t b = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * 8 + (lane >> 3);
+  bool live = b < a.T * nb;
+  const int64_t row = live ? b / nb : 0;
+  const int j = live ? (int)(b - row * nb) : 0;
+  if (a.group_idx && live) {
+    const int g = a.group_idx[row];
+    live = g >= 0 && g < a.G && g == a.group_idx[row & ~(int64_t)(kAlignM - 1)];
   }
-#pragma unroll
-  for (int k = 0; k < U; ++k) {
-    float h[8], g[8], u[8];
-    vh[k].get(h);
-    decode8(cg[k], a.gu_fmt, sg[k], g);
-    decode8(cu[k], a.gu_fmt, su[k], u);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float dz;
-      const float s = act_sigmoid<true>(g[e], a.act, &dz);
-      const float t = s * (1.0f - s);            // zero far from zero, where dz may be infinite
-      const float d = h[e] * u[e] * (t == 0.0f ? s : __builtin_fmaf(g[e] * t, dz, s));
-      u[e] = h[e] * g[e] * s;
-      g[e] = d;
-    }
-    const float s0 = block_scale(block_amax(g), a.fmt), s1 = block_scale(block_amax(u), a.fmt);
-    const uint2 c0 = codes8(g, s0, a.fmt), c1 = codes8(u, s1, a.fmt);
-    if (!live[k]) continue;
-    const int64_t at = row[k] * 2 * a.N + j[k] * kBlockK + 8 * l;
-    *(uint2*)(a.d + at) = c0;
-    *(uint2*)(a.d + at + a.N) = c1;
-    if (l == 0) {
-      a.sd[row[k] * 2 * nb + j[k]] = s0;
-      a.sd[row[k] * 2 * nb + nb + j[k]] = s1;
-    }
+  Eight<BF16> v0, v1;
+  uint4 cg = make_uint4(0, 0, 0, 0), cu = cg;
+  float sg = 1.0f, su = 1.0f;
+  v0.zero();
+  v1.zero();
+  const int64_t at = row * 2 * a.N + j * kBlockK + 16 * l;
+  if (live) {
+    v0.load(a.dh, row * a.N + j * kBlockK + 16 * l);
+    v1.load(a.dh, row * a.N + j * kBlockK + 16 * l + 8);
+    cg = *(const uint4*)(a.gu + at);
+    cu = *(const uint4*)(a.gu + at + a.N);
+    sg = a.sgu[row * 2 * nb + j];
+    su = a.sgu[row * 2 * nb + nb + j];
   }
+  float h[2][8], g[16], u[16];
+  v0.get(h[0]);
+  v1.get(h[1]);
+  decode16(cg, a.gu_fmt, sg, g);
+  decode16(cu, a.gu_fmt, su, u);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    float dz;
+    const float d = h[e >> 3][e & 7], s = act_sigmoid<true>(g[e], ACT, &dz);
+    const float as = g[e] * s, t = 1.0f - s;
+    // t is zero far from zero, where dz may be infinite
+    const float slope = t == 0.0f ? s : __builtin_fmaf(as * t, ACT == kActGelu ? dz : 1.0f, s);
+    g[e] = d * u[e] * (ACT == kActGelu && s == 0.0f ? 0.0f : slope);
+    u[e] = d * as;
+  }
+  const float s0 = scale16(g, a.fmt), s1 = scale16(u, a.fmt);
+  unsigned c0[4], c1[4];
+  codes<16>(g, s0, a.fmt, c0);
+  codes<16>(u, s1, a.fmt, c1);
+  if (!live) return;
+  *(uint4*)(a.d + at) = make_uint4(c0[0], c0[1], c0[2], c0[3]);
+  *(uint4*)(a.d + at + a.N) = make_uint4(c1[0], c1[1], c1[2], c1[3]);
+  if (l == 0) {
+    a.sd[row * 2 * nb + j] = s0;
+    a.sd[row * 2 * nb + nb + j] = s1;
+  }
+}
+
+template <bool BF16>
+void launch_backward(const GatedBackArgs& a, hipStream_t stream) {
+  const int64_t blocks = a.T * (a.N / kBlockK);
+  const dim3 grid((unsigned)((blocks + 31) / 32));
+  if (a.act == kActGelu)
+    hipLaunchKernelGGL((gated_backward_kernel<BF16, kActGelu>), grid, dim3(256), 0, stream, a);
+  else
+    hipLaunchKernelGGL((gated_backward_kernel<BF16, kActSilu>), grid, dim3(256), 0, stream, a);
 }
 
 }  // namespace
@@ -605,14 +620,8 @@ void launch_gated(GatedArgs& a, int kind, int fmt_a, int fmt_b, int num_cus, voi
                       : launch_for<1, 1>(a, kind, num_cus, plan, stream);
 }
 
-void launch_gated_backward(const GatedBackArgs& a, int num_cus, hipStream_t stream) {
-  (void)num_cus;
-  const int64_t blocks = a.T * (a.N / kBlockK), per = 4 * 2 * 4;
-  const dim3 grid((unsigned)((blocks + per - 1) / per));
-  if (a.bf16)
-    hipLaunchKernelGGL(gated_backward_kernel<true>, grid, dim3(256), 0, stream, a);
-  else
-    hipLaunchKernelGGL(gated_backward_kernel<false>, grid, dim3(256), 0, stream, a);
+void launch_gated_backward(const GatedBackArgs& a, hipStream_t stream) {
+  a.bf16 ? launch_backward<true>(a, stream) : launch_backward<false>(a, stream);
 }
 
 }  // namespace dg

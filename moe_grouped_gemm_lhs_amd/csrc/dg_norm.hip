@@ -17,9 +17,12 @@
 namespace dg {
 namespace {
 
-// Eight weights from column c on: bf16, fp32 or ones.
+// Eight weights from column c on: bf16, fp32 or ones; none past the row's end.
 __device__ __forceinline__ void load_weight(const NormArgs& a, int c, float (&w)[8]) {
-  if (!a.w) {
+  if (c >= a.K) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = 0.0f;
+  } else if (!a.w) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) w[e] = 1.0f;
   } else if (a.w_bf16) {
@@ -110,42 +113,52 @@ norm_kernel(NormArgs a) {
 }
 
 // Backward: a workgroup takes rows blockIdx, blockIdx + gridDim, ... and keeps its columns'
-// sums of dy h rstd in registers.
+// weights and sums of dy h rstd in registers.
 template <bool BF16, int NW, int C>
 __global__ void __launch_bounds__(NW * 64)
 norm_backward_kernel(NormArgs a) {
   __shared__ float part[2][NW];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, t = threadIdx.x;
-  float dw[C][8];
+  constexpr bool KEEP = C <= 2;                // longer rows have no registers for the weights
+  float dw[C][8], kept[KEEP ? C : 1][8];
 #pragma unroll
-  for (int i = 0; i < C; ++i)
+  for (int i = 0; i < C; ++i) {
+    const int c = (i * NW * 64 + t) * 8;
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw[i][e] = 0.0f;
+    if (KEEP) load_weight(a, c, kept[i % (KEEP ? C : 1)]);
+  }
+  auto weight = [&](int i, float (&w)[8]) {
+    if constexpr (KEEP) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = kept[i][e];
+    } else {
+      load_weight(a, (i * NW * 64 + t) * 8, w);
+    }
+  };
   int flip = 0;
   for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x, flip ^= 1) {
     const float rstd = a.rstd[row];
-    Eight<BF16> vy[C], vh[C];
+    Eight<BF16> vy[C], vh[C], vg[C];
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       const int c = (i * NW * 64 + t) * 8;
       vy[i].zero();
       vh[i].zero();
+      vg[i].zero();
       if (c < a.K) {
         vy[i].load(a.x, row * a.ldx + c);
         vh[i].load(a.r, row * a.ldr + c);
+        if (KEEP && a.grad_h) vg[i].load(a.grad_h, row * a.ld_gh + c);
       }
     }
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-      const int c = (i * NW * 64 + t) * 8;
       float y[8], h[8], w[8];
       vy[i].get(y);
       vh[i].get(h);
-      if (c < a.K) load_weight(a, c, w);
-      else
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = 0.0f;
+      weight(i, w);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float p = y[e] * h[e];
@@ -164,20 +177,15 @@ norm_backward_kernel(NormArgs a) {
     for (int i = 0; i < C; ++i) {
       const int c = (i * NW * 64 + t) * 8;
       if (c >= a.K) continue;
-      float y[8], h[8], w[8];
+      float y[8], h[8], g[8], w[8];
+      if (!KEEP && a.grad_h) vg[i].load(a.grad_h, row * a.ld_gh + c);
       vy[i].get(y);
       vh[i].get(h);
-      load_weight(a, c, w);
+      vg[i].get(g);
+      weight(i, w);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = rstd * (y[e] * w[e] - h[e] * m);
+      for (int e = 0; e < 8; ++e) y[e] = __builtin_fmaf(rstd, y[e] * w[e] - h[e] * m, g[e]);
       Eight<BF16> o;
-      if (a.grad_h) {
-        float g[8];
-        o.load(a.grad_h, row * a.ld_gh + c);
-        o.get(g);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] += g[e];
-      }
       o.set(y);
       o.store(a.h, row * a.ldh + c);
     }
@@ -193,13 +201,20 @@ norm_backward_kernel(NormArgs a) {
   }
 }
 
-// The workgroups' sums added up: 64 columns a workgroup, 16 waves over its rows.
+// The workgroups' sums added up: 64 columns a workgroup, 16 waves over its rows, eight loads of
+// each in flight.
 __global__ void __launch_bounds__(1024) norm_weight_kernel(const float* partial, float* grad_w, int K, int n) {
   __shared__ float part[16][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = blockIdx.x * 64 + lane;        // K is a multiple of 64
   float sum = 0.0f;
-  for (int i = wave; i < n; i += 16) sum += partial[(int64_t)i * K + c];
+  for (int i = wave; i < n; i += 128) {
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = i + 16 * k < n ? partial[(int64_t)(i + 16 * k) * K + c] : 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum += v[k];
+  }
   part[wave][lane] = sum;
   __syncthreads();
   if (wave == 0) {
@@ -238,7 +253,7 @@ void backward_for(const NormArgs& a, int grid, hipStream_t stream) {
   const int pieces = (a.K + 511) / 512;
   if (pieces <= 4) return launch_back<BF16, 4, 1>(a, grid, stream);
   if (pieces <= 8) return launch_back<BF16, 4, 2>(a, grid, stream);
-  if (pieces <= 16) return launch_back<BF16, 4, 4>(a, grid, stream);
+  if (pieces <= 16) return launch_back<BF16, 8, 2>(a, grid, stream);
   if (pieces <= 32) return launch_back<BF16, 16, 2>(a, grid, stream);
   if (pieces <= 64) return launch_back<BF16, 16, 4>(a, grid, stream);
   return launch_back<BF16, 16, 8>(a, grid, stream);
@@ -246,9 +261,10 @@ void backward_for(const NormArgs& a, int grid, hipStream_t stream) {
 
 }  // namespace
 
-int norm_backward_grid(int64_t T, int64_t K) {
-  (void)K;
-  return (int)(T < kNormMaxGrid ? T : kNormMaxGrid);
+// Two workgroups a CU; of few rows one a CU, and a row each at least.
+int norm_backward_grid(int64_t T) {
+  const int64_t most = T / 4 > 256 ? T / 4 : 256;
+  return (int)(T < most ? T : most < kNormMaxGrid ? most : kNormMaxGrid);
 }
 
 // In slices of rows: a launch has less than 2^32 threads.
@@ -273,7 +289,7 @@ void launch_norm(const NormArgs& args, hipStream_t stream) {
 }
 
 void launch_norm_backward(const NormArgs& a, hipStream_t stream) {
-  const int grid = norm_backward_grid(a.T, a.K);
+  const int grid = norm_backward_grid(a.T);
   if (grid > 0) a.bf16 ? backward_for<true>(a, grid, stream) : backward_for<false>(a, grid, stream);
   if (a.grad_w)
     hipLaunchKernelGGL(norm_weight_kernel, dim3(a.K / 64), dim3(1024), 0, stream, a.partial, a.grad_w, a.K,

@@ -95,7 +95,7 @@ def test_gated_codes(native, kind):
         assert gated(native, kind, GU=A8, sGU=A4) == ALIGN and gated(native, kind, GU=A16, sGU=A2) == ALIGN
 
 
-def back(n, dh=A16, dtype=0, GU=A8, gf=0, sGU=A4, idx=None, act=0, D=A8, sD=A4, fmt=0, T=4, N=256, G=1):
+def back(n, dh=A16, dtype=0, GU=A16, gf=0, sGU=A4, idx=None, act=0, D=A16, sD=A4, fmt=0, T=4, N=256, G=1):
     return n.dg_gated_backward(dh, dtype, GU, gf, sGU, idx, act, D, sD, fmt, T, N, G, None)
 
 
@@ -107,7 +107,7 @@ def test_gated_backward_codes(native):
     assert back(native, T=0, dh=None) == 0 and back(native, N=0, D=None) == 0
     for bad in (dict(dh=None), dict(GU=None), dict(sGU=None), dict(D=None), dict(sD=None)):
         assert back(native, **bad) == NULL, bad
-    for bad in (dict(dh=A8), dict(GU=A4), dict(sGU=A2), dict(D=A4), dict(sD=A2), dict(idx=A2)):
+    for bad in (dict(dh=A8), dict(GU=A8), dict(sGU=A2), dict(D=A8), dict(sD=A2), dict(idx=A2)):
         assert back(native, **bad) == ALIGN, bad
 
 
