@@ -265,11 +265,12 @@ constexpr int kSplitGrid = 256;
 
 // Ranges that W iterations are dealt out to: of four at least (a range costs its first copies'
 // way to memory and the second kernel's reading of its slot), but no longer than a tile.
-__device__ __forceinline__ long split_ranges(long W, int nkb) {
-  const int least = nkb < 4 ? nkb : 4;
-  const long g = udiv(W, least);
+__device__ __forceinline__ unsigned split_ranges(unsigned W, int nkb) {
+  const unsigned g = W / (unsigned)(nkb < 4 ? nkb : 4);
   return g < kSplitGrid ? g : kSplitGrid;
 }
+// First iteration of range g of G.  At most 256 tiles of 2^15 blocks: all of this fits 32 bits.
+__device__ __forceinline__ unsigned split_start(unsigned g, unsigned W, unsigned G) { return g * W / G; }
 
 // The rows under masked_m (dense: all of one group) as the schedule sees them.
 template <class C>
@@ -290,12 +291,12 @@ gated_split_kernel(GatedArgs p) {
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int nkb = p.nkb;
   const MaskedPlan mp = live_tiles<C>(p, lane);
-  const long W = (long)mp.total * nkb;
-  const long G = split_ranges(W, nkb);
-  const long g = blockIdx.x;
-  if (g >= G) return;
-  const long i_begin = stream_start<C>(g, W, G), i_end = stream_start<C>(g + 1, W, G);
-  const int t_first = (int)udiv(i_begin, nkb);
+  const unsigned W = (unsigned)mp.total * nkb, G = split_ranges(W, nkb);
+  // consecutive ranges on one XCD (workgroups go round them): their tiles share rows of A
+  const unsigned each = (G + 7) / 8, g = (blockIdx.x & 7) * each + (blockIdx.x >> 3);
+  if ((blockIdx.x >> 3) >= each || g >= G) return;
+  const unsigned i_begin = split_start(g, W, G), i_end = split_start(g + 1, W, G);
+  const int t_first = (int)(i_begin / (unsigned)nkb);
 
   TileCtx cn;
   cn.A = p.A;
@@ -321,7 +322,7 @@ gated_split_kernel(GatedArgs p) {
 
   // the copies run STAGES - 1 iterations ahead of the products, across the tiles' border
   const int n_iter = (int)(i_end - i_begin);
-  int tc = t_first, kbn = (int)(i_begin - (long)t_first * nkb), kbc = kbn, sn = 0, sc = 0;
+  int tc = t_first, kbn = (int)i_begin - t_first * nkb, kbc = kbn, sn = 0, sc = 0;
   MaskedCursor mn = masked_seek<C>(mp, p.tiles_n, t_first), mc = mn;
   auto at = [&](TileCtx& c, const MaskedCursor& m) {
     masked_tile<C>(p, mp, m, c);
@@ -348,96 +349,141 @@ gated_split_kernel(GatedArgs p) {
     const bool tile_end = kbc == nkb - 1 || step == n_iter - 1;
     if (++kbc == nkb) kbc = 0;
     if (!tile_end) continue;
-    // the sums of this range's part of tile tc, row by row
-    float* slot = p.scratch + (size_t)(g * 2 + (tc != t_first)) * C::BM * C::BN;
-    const __amdgpu_buffer_rsrc_t rw = buffer_over(slot, C::BM * C::BN * 4);
-    const int l32 = lane & 31, half = lane >> 5;
+    // the sums of this range's part of tile tc, as the lanes hold them (1 KB a store)
+    const __amdgpu_buffer_rsrc_t rw =
+        buffer_over(p.scratch + (size_t)(g * 2 + (tc != t_first)) * C::BM * C::BN, C::BM * C::BN * 4);
 #pragma unroll
-    for (int i = 0; i < TI; ++i) {
-      const int r = C::WM * cc.wm + 32 * (i / 2) + l32;
+    for (int i = 0; i < TI; ++i)
 #pragma unroll
-      for (int j = 0; j < TJ; ++j) {                  // see compute_stage_f16
-        const int col = C::WN * cc.wn + 32 * (j / 2) + 8 * (2 * (i & 1) + (j & 1)) + 4 * half;
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i, acc[i][j]), rw,
-                                               r < cc.rows ? (r * C::BN + col) * 4 : kPastTile, 0, 0);
+      for (int j = 0; j < TJ; ++j) {
+        const bool row_ok = C::WM * cc.wm + 32 * (i / 2) + (lane & 31) < cc.rows;
+        __builtin_amdgcn_raw_buffer_store_b128(
+            __builtin_bit_cast(v4i, acc[i][j]), rw,
+            row_ok ? (((wave * TI + i) * TJ + j) * 64 + lane) * 16 : kPastTile, 0, 0);
         acc[i][j] = (v4f){0.f, 0.f, 0.f, 0.f};
       }
-    }
     ++tc;
     if (step < n_iter - 1) masked_next<C>(mp, p.tiles_n, mc);
   }
 }
 
-// A 128-column block of a row is 16 lanes' work, 8 columns each.
+// A workgroup finishes one 128-column block of h for 32 rows: each of its waves adds up the
+// columns that one wave of the first kernel had, held by the lanes as there (compute_stage_f16),
+// so that every load is 1 KB in one piece.
 template <class C>
-__global__ void __launch_bounds__(256)
+struct Finish {
+  static constexpr int HC = C::BN / 2;                // columns of h a tile
+  static constexpr int TILES = kBlockK / HC;
+  static constexpr int W = 4 * TILES;                 // waves
+  static constexpr int NE = C::GW / 8;                // pieces of 4 columns a lane, gate or up
+  static constexpr int GROUPS = C::BM / 32;           // of 32 rows a tile
+};
+
+template <class C>
+__global__ void __launch_bounds__(64 * Finish<C>::W)
 gated_finish_kernel(GatedArgs p) {
-  const int lane = threadIdx.x & 63, l = lane & 15;
+  using F = Finish<C>;
+  constexpr int NE = F::NE, BATCH = NE == 4 ? 4 : 8;  // ranges whose sums are in flight
+  __shared__ unsigned red[3][F::W][32];
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int l32 = lane & 31, half = lane >> 5;
   const int nkb = p.nkb, N = p.N >> 1, nb = N / kBlockK;
+  const int groups = (p.rows + C::BM - 1) / C::BM * F::GROUPS;      // of 32 rows, of the capacity
+  const int block = blockIdx.x % (unsigned)nb, r32 = blockIdx.x / (unsigned)nb;
+  const int grp = r32 / groups, row0 = (r32 - grp * groups) * 32;
   const MaskedPlan mp = live_tiles<C>(p, lane);
-  const long W = (long)mp.total * nkb;
-  const long G = split_ranges(W, nkb);
-  // four blocks a wave, of one row tile or of neighbouring rows
-  const long b = ((long)blockIdx.x * 4 + (threadIdx.x >> 6)) * 4 + (lane >> 4);
-  const long row = udiv(b, nb);                       // of the capacity's
-  const int block = (int)(b - row * nb);
-  const int grp = p.masked_m ? (int)udiv(row, p.rows) : 0;
-  const int r = (int)(row - (long)grp * p.rows);
-  // every lane takes part in the shuffles, whether its row is one or not
-  const int lane_g = grp < 64 ? grp : 63;
-  const int mm = __shfl(mp.mm, lane_g, 64), incl = __shfl(mp.incl, lane_g, 64), rts = __shfl(mp.rt, lane_g, 64);
-  const bool live = grp < (p.masked_m ? p.G : 1) && r < mm;
-  float gate[8], up[8];
+  const int mm = __builtin_amdgcn_readlane(mp.mm, grp);
+  if (row0 >= mm) return;
+  const unsigned W = (unsigned)mp.total * nkb, G = split_ranges(W, nkb);
+  const int tn = block * F::TILES + wave / 4, wn = wave % 4;
+  const unsigned t = (unsigned)(__builtin_amdgcn_readlane(mp.incl, grp) +
+                                (row0 / C::BM - __builtin_amdgcn_readlane(mp.rt, grp)) * p.tiles_n + tn);
+  const unsigned x0 = t * nkb, x1 = x0 + nkb - 1;
+  const int gf = (int)(((x0 + 1) * G + W - 1) / W) - 1, gl = (int)(((x1 + 1) * G + W - 1) / W) - 1, n = gl - gf + 1;
+  // only the first range can begin before the tile, which is then its second
+  const bool second = split_start(gf, W, G) < x0;
+  const int in = row0 % C::BM / 32;                    // the 32-row block of the tile
+  const int wm = in / (C::WM / 32), I = in % (C::WM / 32);
+  const bool live = row0 + l32 < mm;
+  const float* s = p.scratch + (size_t)(gf * 2) * C::BM * C::BN +
+                   (size_t)(wm * C::WAVES_N + wn) * C::TI * C::TJ * 256 + lane * 4;
+  v4f sum[2][NE];                                      // gate, up; piece e: columns 8 e + 4 half
 #pragma unroll
-  for (int e = 0; e < 8; ++e) gate[e] = up[e] = 0.0f;
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int e = 0; e < NE; ++e) sum[k][e] = (v4f){0.f, 0.f, 0.f, 0.f};
   if (live) {
-    const int col = block * kBlockK + 8 * l;           // of h
-    const int tn = col / (C::BN / 2), in = col % (C::BN / 2);
-    const long t = incl - (long)rts * p.tiles_n + (long)(r / C::BM) * p.tiles_n + tn;
-    const long x0 = t * nkb, x1 = x0 + nkb - 1;
-    const long gf = udiv((x0 + 1) * G + W - 1, W) - 1, gl = udiv((x1 + 1) * G + W - 1, W) - 1;
-    // only the first range can begin before the tile, which is then its second
-    const int first = stream_start<C>(gf, W, G) < x0;
-    const int n = (int)(gl - gf) + 1;
-    const float* s = p.scratch + (size_t)(gf * 2) * C::BM * C::BN + (size_t)(r % C::BM) * C::BN +
-                     in / C::GW * C::WN + in % C::GW;
-    constexpr size_t kSlot = (size_t)2 * C::BM * C::BN;
-    for (int k0 = 0; k0 < n; k0 += 4) {
-      v4f a[4][4];                                     // four ranges' loads in flight
+    for (int k0 = 0; k0 < n; k0 += BATCH) {
+      v4f a[BATCH][2][NE];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int i = min(k0 + k, n - 1);
-        const float* at = s + i * kSlot + (i == 0 && first ? kSlot / 2 : 0);
-        a[k][0] = *(const v4f*)at;
-        a[k][1] = *(const v4f*)(at + 4);
-        a[k][2] = *(const v4f*)(at + C::GW);
-        a[k][3] = *(const v4f*)(at + C::GW + 4);
+      for (int b = 0; b < BATCH; ++b) {
+        const int i = min(k0 + b, n - 1);
+        const float* at = s + (size_t)i * 2 * C::BM * C::BN + (i == 0 && second ? C::BM * C::BN : 0);
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int e = 0; e < NE; ++e) {
+            const int c = k * NE + e;                  // piece of the wave's columns, four to 32
+            a[b][k][e] = *(const v4f*)(at + ((2 * I + c % 4 / 2) * C::TJ + 2 * (c / 4) + c % 2) * 256);
+          }
       }
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (k0 + k >= n) break;
+      for (int b = 0; b < BATCH; ++b) {                // selected, not skipped: all loads first
+        const bool on = k0 + b < n;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          gate[e] += a[k][e >> 2][e & 3];
-          up[e] += a[k][2 + (e >> 2)][e & 3];
-        }
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int e = 0; e < NE; ++e)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) sum[k][e][c] += on ? a[b][k][e][c] : 0.0f;
       }
     }
   }
-  float h[8];
+  v4f h[NE];
+  unsigned m[3] = {0, 0, 0};
 #pragma unroll
-  for (int e = 0; e < 8; ++e) h[e] = gate[e] * act_sigmoid<false>(gate[e], p.act, nullptr) * up[e];
-  auto put = [&](const float (&x)[8], uint8_t* codes, float* scale) {
-    const float s = block_scale(block_amax(x), p.out_fmt);
-    const uint2 c = codes8(x, s, p.out_fmt);
-    if (!live) return;
-    *(uint2*)(codes + block * kBlockK + 8 * l) = c;
-    if (l == 0) scale[block] = s;
+  for (int e = 0; e < NE; ++e) {
+    h[e] = gated4(sum[0][e], sum[1][e], p.act);
+    m[0] = magnitude4(h[e], m[0]);
+    m[1] = magnitude4(sum[0][e], m[1]);
+    m[2] = magnitude4(sum[1][e], m[2]);
+  }
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    m[k] = across_halves(m[k]);
+    if (half == 0) red[k][wave][l32] = m[k];
+  }
+  __syncthreads();
+  const size_t row = (size_t)grp * p.rows + row0 + l32;
+  // a swap between the lane halves gives a lane consecutive columns: 16 or 8
+  const int col = block * kBlockK + wave * C::GW + (C::GW / 2) * half;
+  auto put = [&](int plane, const v4f (&v)[NE], uint8_t* codes_at, float* scale_at) {
+    unsigned top = 0;
+#pragma unroll
+    for (int w = 0; w < F::W; ++w) top = umax(top, red[plane][w][l32]);
+    const float scale = block_scale(__builtin_bit_cast(float, top), p.out_fmt);
+    float x[4 * NE];
+    unsigned c[NE];
+#pragma unroll
+    for (int e = 0; e < NE; ++e)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[4 * e + k] = v[e][k];
+    codes<4 * NE>(x, scale, p.out_fmt, c);
+    if constexpr (NE == 4) {
+      const auto a = __builtin_amdgcn_permlane32_swap(c[0], c[2], false, false);
+      const auto b = __builtin_amdgcn_permlane32_swap(c[1], c[3], false, false);
+      if (live) *(uint4*)(codes_at + col) = make_uint4(a[0], a[1], b[0], b[1]);
+    } else {
+      const auto a = __builtin_amdgcn_permlane32_swap(c[0], c[1], false, false);
+      if (live) *(uint2*)(codes_at + col) = make_uint2(a[0], a[1]);
+    }
+    if (live && wave == 0 && half == 0) scale_at[block] = scale;
   };
-  put(h, p.H + row * N, p.sH + row * nb);
+  put(0, h, p.H + row * N, p.sH + row * nb);
   if (!p.GU) return;
-  put(gate, p.GU + row * 2 * N, p.sGU + row * 2 * nb);
-  put(up, p.GU + row * 2 * N + N, p.sGU + row * 2 * nb + nb);
+  put(1, sum[0], p.GU + row * 2 * N, p.sGU + row * 2 * nb);
+  put(2, sum[1], p.GU + row * 2 * N + N, p.sGU + row * 2 * nb + nb);
 }
 
 template <int FA, int FB> using Tile = GatedCfg<Cfg<128, 256, 2, 4, 3, false, FA, FB, 4>>;
@@ -458,8 +504,9 @@ template <class C, class F>
 void launch_split(GatedArgs& a, int kind, hipStream_t stream) {
   a.tiles_n = a.N / C::BN;
   hipLaunchKernelGGL(gated_split_kernel<C>, dim3(kSplitGrid), dim3(C::NT), 0, stream, a);
-  const int64_t blocks = (int64_t)a.rows * (kind == kMasked ? a.G : 1) * (a.N / 2 / kBlockK);
-  hipLaunchKernelGGL(gated_finish_kernel<F>, dim3((unsigned)((blocks + 15) / 16)), dim3(256), 0, stream, a);
+  const int row_tiles = (a.rows + C::BM - 1) / C::BM * (kind == kMasked ? a.G : 1);
+  hipLaunchKernelGGL(gated_finish_kernel<F>, dim3(row_tiles * Finish<F>::GROUPS * (a.N / 2 / kBlockK)),
+                     dim3(64 * Finish<F>::W), 0, stream, a);
 }
 
 template <int FA, int FB>
