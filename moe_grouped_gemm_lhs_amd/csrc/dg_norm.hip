@@ -236,6 +236,7 @@ void forward_for(const NormArgs& a, hipStream_t stream) {
   const int pieces = (a.K + 511) / 512;        // of 512 values, a wave's worth
   if (pieces <= 1) return launch_forward<BF16, 1, 1>(a, stream);
   if (pieces <= 4) return launch_forward<BF16, 4, 1>(a, stream);
+  if (a.T <= 512 && pieces <= 16) return launch_forward<BF16, 16, 1>(a, stream);
   if (pieces <= 8) return launch_forward<BF16, 4, 2>(a, stream);
   if (pieces <= 16) return launch_forward<BF16, 4, 4>(a, stream);
   if (pieces <= 32) return launch_forward<BF16, 16, 2>(a, stream);

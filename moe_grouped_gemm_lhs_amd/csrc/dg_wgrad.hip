@@ -95,16 +95,25 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_over(const void* base, 
 
 // Every step-th of the 128-row blocks of a group (those whose first row names it), from the
 // skip-th on; without groups, of all blocks.
+// 256 of them are looked at at a time: the look waits for memory, and with it for every copy
+// in flight.
 template <bool GROUPED>
 struct Blocks {
   const int32_t* idx;
   int g, lane;
   int end, step, skip;
-  int b;                           // the 64 blocks in `mask` are b .. b + 63; without groups the next
-  uint64_t mask;
+  int b;                           // the blocks in masks are b .. b + 255; without groups the next
+  uint64_t mask[4];
   __device__ __forceinline__ void look() {
-    const int at = b + lane;
-    mask = __builtin_amdgcn_ballot_w64(at < end && idx[(int64_t)at * kAlignM] == g);
+    int lead[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int at = b + 64 * k + lane;
+      lead[k] = idx[(int64_t)(at < end ? at : 0) * kAlignM];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      mask[k] = __builtin_amdgcn_ballot_w64(b + 64 * k + lane < end && lead[k] == g);
   }
   __device__ __forceinline__ int next() {       // -1: none left
     if (!GROUPED) {
@@ -113,13 +122,19 @@ struct Blocks {
       return at < end ? at : -1;
     }
     for (;;) {
-      while (mask == 0) {
-        b += 64;
+      while ((mask[0] | mask[1] | mask[2] | mask[3]) == 0) {
+        b += 256;
         if (b >= end) return -1;
         look();
       }
-      const int i = (int)__builtin_ctzll(mask);
-      mask &= mask - 1;
+      const int k = mask[0] ? 0 : mask[1] ? 1 : mask[2] ? 2 : 3;
+      uint64_t m = mask[0] ? mask[0] : mask[1] ? mask[1] : mask[2] ? mask[2] : mask[3];
+      const int i = 64 * k + (int)__builtin_ctzll(m);
+      m &= m - 1;
+      if (k == 0) mask[0] = m;
+      if (k == 1) mask[1] = m;
+      if (k == 2) mask[2] = m;
+      if (k == 3) mask[3] = m;
       if (skip-- > 0) continue;
       skip = step - 1;
       return b + i;
@@ -289,7 +304,10 @@ __global__ void __launch_bounds__(512) wgrad_kernel(WgradArgs a) {
   blocks.step = a.splits;
   blocks.skip = split;
   blocks.b = GROUPED ? 0 : split;
-  if (GROUPED) blocks.look();
+  if (GROUPED && nblocks > 0)
+    blocks.look();
+  else
+    blocks.mask[0] = blocks.mask[1] = blocks.mask[2] = blocks.mask[3] = 0;
   // First row of the next step, or -1: a block is two steps, the second unless it is empty.
   int64_t block_row = -1;
   auto next_step = [&]() -> int64_t {

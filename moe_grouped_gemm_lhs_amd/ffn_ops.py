@@ -106,24 +106,33 @@ def dg_rms_norm_fp8(X, weight=None, *, residual=None, eps=1e-6, fmt="e4m3", code
     new tensor or the given one, which may be X or residual.  Row strides are multiples of 8 and
     matrices start on 16 bytes.  Nothing that is returned carries a gradient."""
     native = moe_ops._native or _load_native()
-    dev = _device(X, "X")
-    if _away(dev, stream):
-        with binding._elsewhere(dev, stream):
+    dev, dtype = X.device, X.dtype
+    index = dev.index
+    if stream is not None or index is None or index != torch._C._cuda_getDevice():
+        with binding._elsewhere(_device(X, "X"), stream):
             return dg_rms_norm_fp8(X, weight, residual=residual, eps=eps, fmt=fmt, codes=codes, bf16=bf16,
                                    save=save, Q=Q, S=S, H=H, Y=Y, rstd=rstd)
-    dtype, code = X.dtype, _in_dtype(X, "X")
-    if X.dim() != 2:
+    code = _IN_DTYPES.get(dtype)
+    if code is None:
+        raise TypeError(f"X must be float32 or bfloat16, got {dtype}")
+    shape = X.shape
+    if len(shape) != 2:
         raise ValueError("X must be 2-D (T x K)")
-    shape = T, K = X.shape
+    T, K = shape
     p_x, ldx = native.rows(X, "X", dtype, shape, dev)
-    p_w, w_code = _weight(native, weight, K, dev)
-    fmt_code = _format(fmt)
+    p_w, w_code = (None, 0) if weight is None else _weight(native, weight, K, dev)
+    fmt_code = _FORMATS.get(fmt)
+    if fmt_code is None:
+        raise ValueError(f"unknown fp8 format {fmt!r}")
     p_q = p_s = p_r = p_h = p_y = None
     ldr = ldh = ldy = 0
     if codes:
-        Q = _codes_out(Q, "Q", fmt, shape, dev)
-        S = _scales_out(S, (T, K // 128), dev)
-        p_q = native.vector(Q, "Q", Q.dtype, shape, dev)
+        fp8 = _FP8_OF[fmt]
+        if Q is None or Q.dtype is not fp8:
+            Q = _codes_out(Q, "Q", fmt, shape, dev)
+        if S is None:
+            S = torch.empty((T, K // 128), dtype=torch.float32, device=dev)
+        p_q = native.vector(Q, "Q", fp8, shape, dev)
         p_s = native.vector(S, "S", torch.float32, (T, K // 128), dev)
     elif Q is not None or S is not None:
         raise ValueError("Q and S are written with codes=True")
@@ -144,7 +153,7 @@ def dg_rms_norm_fp8(X, weight=None, *, residual=None, eps=1e-6, fmt="e4m3", code
         rstd = torch.empty((T,), dtype=torch.float32, device=dev)
     p_rstd = native.vector(rstd, "rstd", torch.float32, (T,), dev)
     st = native.dg_rms_norm_fp8(p_x, code, ldx, p_r, ldr, p_w, w_code, eps, p_h, ldh, p_q, p_s, fmt_code, p_y,
-                                ldy, p_rstd, T, K, torch._C._cuda_getCurrentRawStream(dev.index))
+                                ldy, p_rstd, T, K, torch._C._cuda_getCurrentRawStream(index))
     if st != 0:
         raise DGError(st, "dg_rms_norm_fp8")
     return Q, S, H, Y, rstd
