@@ -392,6 +392,12 @@ def _transposed(codes, scales):
     return binding.dg_transpose_fp8(codes), scales.t().contiguous()
 
 
+def _dense(grad):
+    """A gradient as the calls take it; torch's may be broadcast, turned or a part of another."""
+    grad = grad.contiguous()
+    return grad if grad.data_ptr() % 16 == 0 else grad.clone()
+
+
 class _GatedFFN(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, residual, norm_weight, w13, w2, eps, activation):
@@ -412,7 +418,8 @@ class _GatedFFN(torch.autograd.Function):
         need = ctx.needs_input_grad
         if grad_out is None:
             return (grad_h, grad_h if ctx.has_residual else None) + (None,) * 5
-        d, sd = binding.dg_quantize_fp8_1x128(grad_out.contiguous())
+        grad_h = None if grad_h is None else _dense(grad_h)
+        d, sd = binding.dg_quantize_fp8_1x128(_dense(grad_out))
         da = binding.dg_gemm_fp8_nt(d, sd, *_transposed(b2, s2))
         dw2 = dg_wgrad_fp8(d, sd, a, sa, dtype=ctx.dtypes[1]) if need[4] else None
         d, sd = dg_gated_backward(da, gu, sgu, activation=ctx.activation)
@@ -433,5 +440,6 @@ def gated_ffn(x, w13, w2, *, residual=None, norm_weight=None, eps=1e-6, activati
     kept for the backward pass is the stream x + residual and codes.
 
     Returns (out T x M bfloat16, x + residual or None without a residual), differentiable once
-    by x, residual, norm_weight, w13 and w2."""
+    by x, residual, norm_weight, w13 and w2.  A step may be captured in a graph, if no graph of
+    autograd's that was built outside the capture on the same leaves is alive then."""
     return _GatedFFN.apply(x, residual, norm_weight, w13, w2, eps, activation)
