@@ -255,33 +255,49 @@ __device__ __forceinline__ void gated_step(uint8_t* __restrict__ next, const uin
 }
 
 // ------------------------------------------------------------------------------------
-// Few tiles (decode, experts with few rows): the (tile, K block) iterations of the tiles that
-// have rows, tile after tile, are dealt out evenly to kSplitGrid workgroups, so that every CU
-// streams the same share of B.  There are no more tiles than workgroups, so a workgroup's range
-// lies in at most two tiles; it leaves the fp32 sums of each in a slot of its own in the
-// workspace, and a second kernel adds the slots of a tile in their order, forms h and quantises
-// it.  Nothing waits, and nothing in the workspace need be cleared.
+// Few tiles (decode, experts with few rows).  A row tile has L = tiles_n nkb iterations, tile after
+// tile of its columns and K block after K block; each of the R row tiles that have rows gets
+// Q = kSplitGrid / R workgroups, which share its iterations evenly, so that every CU streams the
+// same share of B.  A group's row tiles are cut at the same places, and the workgroups of one
+// piece run side by side on one XCD: B comes from memory once for all of them.  There are no more
+// tiles than workgroups, so a workgroup's piece lies in at most two tiles; it leaves the fp32 sums
+// of each in a slot of its own in the workspace, and a second kernel adds the slots of a tile in
+// their order, forms h and quantises it.  Nothing waits, and nothing in the workspace need be cleared.
 constexpr int kSplitGrid = 256;
 
-// Ranges that W iterations are dealt out to: of four at least (a range costs its first copies'
-// way to memory and the second kernel's reading of its slot), but no longer than a tile.
-__device__ __forceinline__ unsigned split_ranges(unsigned W, int nkb) {
-  const unsigned g = W / (unsigned)(nkb < 4 ? nkb : 4);
-  return g < kSplitGrid ? g : kSplitGrid;
-}
-// First iteration of range g of G.  At most 256 tiles of 2^15 blocks: all of this fits 32 bits.
-__device__ __forceinline__ unsigned split_start(unsigned g, unsigned W, unsigned G) { return g * W / G; }
-
-// The rows under masked_m (dense: all of one group) as the schedule sees them.
+struct SplitPlan {
+  int mm;                        // this lane's group: rows under masked_m (dense: one group, all rows)
+  int rt;                        // its row tiles
+  int incl;                      // row tiles of groups 0 .. lane
+  unsigned L, Q;                 // iterations of a row tile, pieces that they are cut into
+  int total;                     // workgroups
+};
 template <class C>
-__device__ __forceinline__ MaskedPlan live_tiles(const GatedArgs& p, int lane) {
-  if (p.masked_m) return masked_plan<C>(p, lane);
-  MaskedPlan m;
-  m.mm = lane == 0 ? p.rows : 0;
-  m.rt = (m.mm + C::BM - 1) / C::BM;
-  m.incl = m.total = ((p.rows + C::BM - 1) / C::BM) * p.tiles_n;
+__device__ __forceinline__ SplitPlan split_plan(const GatedArgs& p, int lane) {
+  SplitPlan m;
+  int v = !p.masked_m ? (lane == 0 ? p.rows : 0) : lane < p.G ? p.masked_m[lane] : 0;
+  v = v < 0 ? 0 : (v > p.rows ? p.rows : v);
+  m.mm = v;
+  m.rt = (v + C::BM - 1) / C::BM;
+  int incl = m.rt;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int u = __shfl_up(incl, off, 64);
+    if (lane >= off) incl += u;
+  }
+  m.incl = incl;
+  const int R = __builtin_amdgcn_readlane(incl, 63);
+  // pieces of four iterations at least (one costs its first copies' way to memory and the second
+  // kernel's reading of its slot), but no longer than a tile
+  m.L = (unsigned)p.tiles_n * p.nkb;
+  const unsigned most = m.L / (unsigned)(p.nkb < 4 ? p.nkb : 4);
+  m.Q = R > 0 ? kSplitGrid / (unsigned)R : 0;
+  m.Q = m.Q < most ? m.Q : most;
+  m.total = (int)m.Q * R;
   return m;
 }
+// First iteration of piece j.  At most 256 tiles of 2^15 blocks: all of this fits 32 bits.
+__device__ __forceinline__ unsigned piece_start(const SplitPlan& m, unsigned j) { return j * m.L / m.Q; }
 
 template <class C>
 __global__ void __launch_bounds__(C::NT)
@@ -290,12 +306,16 @@ gated_split_kernel(GatedArgs p) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[STAGES * C::STAGE_BYTES];
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int nkb = p.nkb;
-  const MaskedPlan mp = live_tiles<C>(p, lane);
-  const unsigned W = (unsigned)mp.total * nkb, G = split_ranges(W, nkb);
-  // consecutive ranges on one XCD (workgroups go round them): their tiles share rows of A
-  const unsigned each = (G + 7) / 8, g = (blockIdx.x & 7) * each + (blockIdx.x >> 3);
-  if ((blockIdx.x >> 3) >= each || g >= G) return;
-  const unsigned i_begin = split_start(g, W, G), i_end = split_start(g + 1, W, G);
+  const SplitPlan mp = split_plan<C>(p, lane);
+  // consecutive ones on one XCD (workgroups go round them)
+  const unsigned each = (mp.total + 7) / 8, s = (blockIdx.x & 7) * each + (blockIdx.x >> 3);
+  if ((blockIdx.x >> 3) >= each || s >= (unsigned)mp.total) return;
+  const int g = (int)__builtin_popcountll(__builtin_amdgcn_ballot_w64(mp.incl * (int)mp.Q <= (int)s));
+  const int rt = __builtin_amdgcn_readlane(mp.rt, g), mm = __builtin_amdgcn_readlane(mp.mm, g);
+  const unsigned o = s - (__builtin_amdgcn_readlane(mp.incl, g) - rt) * mp.Q;
+  const unsigned j = o / (unsigned)rt;
+  const int row0 = (int)(o - j * rt) * C::BM;
+  const unsigned i_begin = piece_start(mp, j), i_end = piece_start(mp, j + 1);
   const int t_first = (int)(i_begin / (unsigned)nkb);
 
   TileCtx cn;
@@ -313,35 +333,42 @@ gated_split_kernel(GatedArgs p) {
   cn.wn = wave - cn.wm * C::WAVES_N;
   cn.q = lane >> 4;
   cn.l16 = lane & 15;
+  cn.a_row0 = g * p.rows + row0;
+  cn.rows = min(C::BM, mm - row0);
+  cn.Bg = p.B + (size_t)g * p.N * p.K;
+  cn.sBg = p.sB + (size_t)g * p.nnb * nkb;
+  auto tile = [](TileCtx& c, int t) {
+    c.n0 = t * C::BN;
+    c.nb_first = c.n0 / (2 * kBlockK);
+  };
+  tile(cn, t_first);
   TileCtx cc = cn;
   v4f acc[TI][TJ];
 #pragma unroll
   for (int i = 0; i < TI; ++i)
 #pragma unroll
     for (int j = 0; j < TJ; ++j) acc[i][j] = (v4f){0.f, 0.f, 0.f, 0.f};
+  // waves past the last row only copy: 16 rows of 8 groups, (2048, 7168), 50 us against 60
+  const bool computes = C::WM * cc.wm < cc.rows;
 
   // the copies run STAGES - 1 iterations ahead of the products, across the tiles' border
   const int n_iter = (int)(i_end - i_begin);
-  int tc = t_first, kbn = (int)i_begin - t_first * nkb, kbc = kbn, sn = 0, sc = 0;
-  MaskedCursor mn = masked_seek<C>(mp, p.tiles_n, t_first), mc = mn;
-  auto at = [&](TileCtx& c, const MaskedCursor& m) {
-    masked_tile<C>(p, mp, m, c);
-    c.nb_first = c.n0 / (2 * kBlockK);
-  };
+  int tn = t_first, tc = t_first, kbn = (int)i_begin - t_first * nkb, kbc = kbn, sn = 0, sc = 0;
   for (int step = 1 - STAGES; step < n_iter; ++step) {
     if (step >= 0) {
       wait_stage_copies<C, STAGES - 2>(wave, min(STAGES - 2, n_iter - 1 - step));
       stage_barrier();
     }
     const bool issue = step + STAGES - 1 < n_iter;
-    at(cn, mn);
-    at(cc, mc);
-    gated_step<C>(smem + sn * C::STAGE_BYTES, smem + sc * C::STAGE_BYTES, cn, issue, kbn, cc, step >= 0, acc);
+    tile(cn, tn);
+    tile(cc, tc);
+    gated_step<C>(smem + sn * C::STAGE_BYTES, smem + sc * C::STAGE_BYTES, cn, issue, kbn, cc,
+                  step >= 0 && computes, acc);
     if (issue) {
       sn = sn + 1 == STAGES ? 0 : sn + 1;
       if (++kbn == nkb) {
         kbn = 0;
-        if (step + STAGES < n_iter) masked_next<C>(mp, p.tiles_n, mn);
+        ++tn;
       }
     }
     if (step < 0) continue;
@@ -349,9 +376,9 @@ gated_split_kernel(GatedArgs p) {
     const bool tile_end = kbc == nkb - 1 || step == n_iter - 1;
     if (++kbc == nkb) kbc = 0;
     if (!tile_end) continue;
-    // the sums of this range's part of tile tc, as the lanes hold them (1 KB a store)
+    // the sums of this piece's part of tile tc, as the lanes hold them (1 KB a store)
     const __amdgpu_buffer_rsrc_t rw =
-        buffer_over(p.scratch + (size_t)(g * 2 + (tc != t_first)) * C::BM * C::BN, C::BM * C::BN * 4);
+        buffer_over(p.scratch + (size_t)(s * 2 + (tc != t_first)) * C::BM * C::BN, C::BM * C::BN * 4);
 #pragma unroll
     for (int i = 0; i < TI; ++i)
 #pragma unroll
@@ -363,62 +390,62 @@ gated_split_kernel(GatedArgs p) {
         acc[i][j] = (v4f){0.f, 0.f, 0.f, 0.f};
       }
     ++tc;
-    if (step < n_iter - 1) masked_next<C>(mp, p.tiles_n, mc);
   }
 }
 
-// A workgroup finishes one 128-column block of h for 32 rows: each of its waves adds up the
-// columns that one wave of the first kernel had, held by the lanes as there (compute_stage_f16),
-// so that every load is 1 KB in one piece.
+// A workgroup finishes one 128-column block of h for 16 rows: each of its waves adds up the
+// columns that one wave of the first kernel had, held by the lanes as there (compute_stage_f16)
+// but for bit 4: those lanes add up every other range of the same rows, so that a wave has twice
+// as many loads in flight.
 template <class C>
 struct Finish {
   static constexpr int HC = C::BN / 2;                // columns of h a tile
   static constexpr int TILES = kBlockK / HC;
   static constexpr int W = 4 * TILES;                 // waves
   static constexpr int NE = C::GW / 8;                // pieces of 4 columns a lane, gate or up
-  static constexpr int GROUPS = C::BM / 32;           // of 32 rows a tile
+  static constexpr int GROUPS = C::BM / 16;           // of 16 rows a tile
 };
 
 template <class C>
 __global__ void __launch_bounds__(64 * Finish<C>::W)
 gated_finish_kernel(GatedArgs p) {
   using F = Finish<C>;
-  constexpr int NE = F::NE, BATCH = NE == 4 ? 4 : 8;  // ranges whose sums are in flight
-  __shared__ unsigned red[3][F::W][32];
+  constexpr int NE = F::NE, BATCH = NE == 4 ? 3 : 5;  // ranges whose sums a lane has in flight
+  __shared__ unsigned red[3][F::W][16];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  const int l32 = lane & 31, half = lane >> 5;
+  const int l16 = lane & 15, odd = (lane >> 4) & 1, half = lane >> 5;
   const int nkb = p.nkb, N = p.N >> 1, nb = N / kBlockK;
-  const int groups = (p.rows + C::BM - 1) / C::BM * F::GROUPS;      // of 32 rows, of the capacity
-  const int block = blockIdx.x % (unsigned)nb, r32 = blockIdx.x / (unsigned)nb;
-  const int grp = r32 / groups, row0 = (r32 - grp * groups) * 32;
-  const MaskedPlan mp = live_tiles<C>(p, lane);
+  const int groups = (p.rows + C::BM - 1) / C::BM * F::GROUPS;      // of 16 rows, of the capacity
+  const int block = blockIdx.x % (unsigned)nb, r16 = blockIdx.x / (unsigned)nb;
+  const int grp = r16 / groups, row0 = (r16 - grp * groups) * 16;
+  const SplitPlan mp = split_plan<C>(p, lane);
   const int mm = __builtin_amdgcn_readlane(mp.mm, grp);
   if (row0 >= mm) return;
-  const unsigned W = (unsigned)mp.total * nkb, G = split_ranges(W, nkb);
   const int tn = block * F::TILES + wave / 4, wn = wave % 4;
-  const unsigned t = (unsigned)(__builtin_amdgcn_readlane(mp.incl, grp) +
-                                (row0 / C::BM - __builtin_amdgcn_readlane(mp.rt, grp)) * p.tiles_n + tn);
-  const unsigned x0 = t * nkb, x1 = x0 + nkb - 1;
-  const int gf = (int)(((x0 + 1) * G + W - 1) / W) - 1, gl = (int)(((x1 + 1) * G + W - 1) / W) - 1, n = gl - gf + 1;
-  // only the first range can begin before the tile, which is then its second
-  const bool second = split_start(gf, W, G) < x0;
+  const unsigned x0 = (unsigned)tn * nkb, x1 = x0 + nkb - 1;
+  const int jf = (int)(((x0 + 1) * mp.Q + mp.L - 1) / mp.L) - 1, jl = (int)(((x1 + 1) * mp.Q + mp.L - 1) / mp.L) - 1;
+  const int n = jl - jf + 1, rt = __builtin_amdgcn_readlane(mp.rt, grp);
+  const int slot = (__builtin_amdgcn_readlane(mp.incl, grp) - rt) * (int)mp.Q + jf * rt + row0 / C::BM;
+  const int next = 2 * rt * C::BM * C::BN;             // the row tile's next piece
+  // only the first piece can begin before the tile, which is then its second
+  const bool second = piece_start(mp, jf) < x0;
   const int in = row0 % C::BM / 32;                    // the 32-row block of the tile
   const int wm = in / (C::WM / 32), I = in % (C::WM / 32);
-  const bool live = row0 + l32 < mm;
-  const float* s = p.scratch + (size_t)(gf * 2) * C::BM * C::BN +
-                   (size_t)(wm * C::WAVES_N + wn) * C::TI * C::TJ * 256 + lane * 4;
+  const bool live = row0 + l16 < mm;
+  const float* s = p.scratch + (size_t)(slot * 2) * C::BM * C::BN +
+                   (size_t)(wm * C::WAVES_N + wn) * C::TI * C::TJ * 256 + (32 * half + row0 % 32 + l16) * 4;
   v4f sum[2][NE];                                      // gate, up; piece e: columns 8 e + 4 half
 #pragma unroll
   for (int k = 0; k < 2; ++k)
 #pragma unroll
     for (int e = 0; e < NE; ++e) sum[k][e] = (v4f){0.f, 0.f, 0.f, 0.f};
   if (live) {
-    for (int k0 = 0; k0 < n; k0 += BATCH) {
+    for (int k0 = odd; k0 < n; k0 += 2 * BATCH) {
       v4f a[BATCH][2][NE];
 #pragma unroll
       for (int b = 0; b < BATCH; ++b) {
-        const int i = min(k0 + b, n - 1);
-        const float* at = s + (size_t)i * 2 * C::BM * C::BN + (i == 0 && second ? C::BM * C::BN : 0);
+        const int i = min(k0 + 2 * b, n - 1);
+        const float* at = s + (int64_t)i * next + (i == 0 && second ? C::BM * C::BN : 0);
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -430,7 +457,7 @@ gated_finish_kernel(GatedArgs p) {
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int b = 0; b < BATCH; ++b) {                // selected, not skipped: all loads first
-        const bool on = k0 + b < n;
+        const bool on = k0 + 2 * b < n;
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -440,6 +467,16 @@ gated_finish_kernel(GatedArgs p) {
       }
     }
   }
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int e = 0; e < NE; ++e)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {                    // even and odd ranges, in both lanes
+        const unsigned v = __float_as_uint(sum[k][e][c]);
+        const auto w = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        sum[k][e][c] = __uint_as_float(w[0]) + __uint_as_float(w[1]);
+      }
   v4f h[NE];
   unsigned m[3] = {0, 0, 0};
 #pragma unroll
@@ -452,16 +489,17 @@ gated_finish_kernel(GatedArgs p) {
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
     m[k] = across_halves(m[k]);
-    if (half == 0) red[k][wave][l32] = m[k];
+    if (lane < 16) red[k][wave][l16] = m[k];
   }
   __syncthreads();
-  const size_t row = (size_t)grp * p.rows + row0 + l32;
+  const size_t row = (size_t)grp * p.rows + row0 + l16;
+  const bool store = live && odd == 0;
   // a swap between the lane halves gives a lane consecutive columns: 16 or 8
   const int col = block * kBlockK + wave * C::GW + (C::GW / 2) * half;
   auto put = [&](int plane, const v4f (&v)[NE], uint8_t* codes_at, float* scale_at) {
     unsigned top = 0;
 #pragma unroll
-    for (int w = 0; w < F::W; ++w) top = umax(top, red[plane][w][l32]);
+    for (int w = 0; w < F::W; ++w) top = umax(top, red[plane][w][l16]);
     const float scale = block_scale(__builtin_bit_cast(float, top), p.out_fmt);
     float x[4 * NE];
     unsigned c[NE];
@@ -473,12 +511,12 @@ gated_finish_kernel(GatedArgs p) {
     if constexpr (NE == 4) {
       const auto a = __builtin_amdgcn_permlane32_swap(c[0], c[2], false, false);
       const auto b = __builtin_amdgcn_permlane32_swap(c[1], c[3], false, false);
-      if (live) *(uint4*)(codes_at + col) = make_uint4(a[0], a[1], b[0], b[1]);
+      if (store) *(uint4*)(codes_at + col) = make_uint4(a[0], a[1], b[0], b[1]);
     } else {
       const auto a = __builtin_amdgcn_permlane32_swap(c[0], c[1], false, false);
-      if (live) *(uint2*)(codes_at + col) = make_uint2(a[0], a[1]);
+      if (store) *(uint2*)(codes_at + col) = make_uint2(a[0], a[1]);
     }
-    if (live && wave == 0 && half == 0) scale_at[block] = scale;
+    if (store && wave == 0 && half == 0) scale_at[block] = scale;
   };
   put(0, h, p.H + row * N, p.sH + row * nb);
   if (!p.GU) return;
@@ -631,22 +669,30 @@ void launch_backward(const GatedBackArgs& a, hipStream_t stream) {
 }  // namespace
 
 // Whole tiles or split ones, by what either takes (microseconds, fitted to both sides measured
-// at 1 to 256 rows, dense, and 72 to 1024 rows of 1 to 8 groups).  Whole tiles: 1.55 for each K block,
-// in as many rounds as the tiles need; 64 rows of (2048, 7168) 84, of (16384, 512) 12.8.  Split: two
-// launches, the same work spread over the GPU (half of it in tiles of 64 rows) at 2.0 a block, and
-// the sums' way to memory and back: 64 rows of (2048, 7168) 21.5, of (16384, 512) 15.6; 128 rows
-// of (12288, 1536) 32 against 24.
+// at 1 to 1000 rows of 1 to 16 groups, K 512 to 7168).  Whole tiles, one a CU: a start and 1.45 for
+// each K block; 512 12.3 (measured 12.8), 2048 29.7 (29.5), 4096 52.9 (52 to 61), 7168 87.7 (86
+// to 93).  Split: two launches, 2.0 for each iteration of a piece (half of it in tiles of 64 rows),
+// and the sums' way to the caches and back: 64 rows of (2048, 7168) 20.9 (20.6; whole 84), 500 of
+// (2048, 2048) 28.2 (28.0; whole 29.7), 128 of (12288, 1536) 30.2 (28.7; whole 24.6).  The masked
+// form's counts are not known here: the mean over all of them up to the capacity is taken for
+// them (4 groups of 200 rows, (2048, 4096): 23 to 46 us from a tenth of the rows to all, whole 52 to 55).
 GatedPlan gated_plan(int kind, int64_t rows, int64_t N, int64_t K, int64_t G) {
   GatedPlan p{};
   if (kind == kContiguous || (kind == kMasked && G > 64)) return p;
   const int64_t groups = kind == kMasked ? G : 1;
   const int bm = rows <= 64 ? 64 : 128, cols = bm == 64 ? 64 : 128;
-  const int64_t tiles = (rows + bm - 1) / bm * groups * (N / cols);
-  if (tiles > kSplitGrid) return p;
-  const double nkb = (double)(K / kBlockK), t128 = (double)((rows + 127) / 128 * groups * (N / kBlockK));
-  const double whole = 3 + 1.55 * nkb;
-  const double sums = 2.0 * 8 * N * rows * groups * (kSplitGrid / t128 + 1);     // bytes, there and back
-  const double split = 11 + 2.0 * nkb * t128 / kSplitGrid * (bm == 64 ? 0.5 : 1) + sums / 5.4e6;
+  if ((rows + bm - 1) / bm * groups * (N / cols) > kSplitGrid) return p;
+  // a group's rows and row tiles
+  const double full = (double)(rows / bm), rest = (double)(rows % bm);
+  const double mean_rows = kind == kMasked ? 0.5 * (rows + 1) : (double)rows;
+  const double row_tiles =
+      kind == kMasked ? (0.5 * bm * full + rest) * (full + 1) / rows : (double)((rows + bm - 1) / bm);
+  const double nkb = (double)(K / kBlockK), tiles = row_tiles * groups * (N / cols);
+  double pieces = kSplitGrid / tiles;                          // of a tile
+  if (pieces > nkb / 4) pieces = nkb < 4 ? 1 : nkb / 4;
+  const double sums = 2.0 * 8 * N * mean_rows * groups * (pieces + 1);       // bytes, there and back
+  const double whole = 6.5 + 1.45 * nkb;
+  const double split = 12 + (bm == 64 ? 1 : 2) * nkb / pieces + sums / 10e6;
   if (whole <= split) return p;
   p.bm = bm;
   p.bytes = (size_t)kSplitGrid * 2 * bm * (2 * cols) * 4;
