@@ -8,6 +8,10 @@
 // Memory-bound: every value is loaded once, in 16-byte accesses, and stays in registers
 // between the row's sum and its use.  NW waves share a row and each lane holds C pieces of
 // 8 values, 64 NW 8 apart, so 16 lanes hold one 128-block.
+//
+// Forward, 4096 x 7168 bf16 with a residual: 56 us for 265 MB, 4.7 TB/s (a copy of 256 MB: 5.4); one
+// row 2.8 us, of which an empty launch takes 1.6.  Backward, 8192 x 7168 bf16 with both incoming
+// gradients: 92 us for 470 MB, 5.1 TB/s, and 4.8 for the weight's sums.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -113,7 +117,9 @@ norm_kernel(NormArgs a) {
 }
 
 // Backward: a workgroup takes rows blockIdx, blockIdx + gridDim, ... and keeps its columns'
-// weights and sums of dy h rstd in registers.
+// weights and sums of dy h rstd in registers.  The weights loaded again for each row, four pieces a
+// lane and 1024 workgroups, whose rows of sums the second kernel reads, took 120 + 21 us of 8192 x
+// 7168, where this takes 92 + 4.8.
 template <bool BF16, int NW, int C>
 __global__ void __launch_bounds__(NW * 64)
 norm_backward_kernel(NormArgs a) {
@@ -233,6 +239,9 @@ void launch_forward(const NormArgs& a, hipStream_t stream) {
 
 template <bool BF16>
 void forward_for(const NormArgs& a, hipStream_t stream) {
+  // Few rows leave waves idle unless a row has 16 (7168 values: one row 3.1 us against 4.5, 256 rows 4.5
+  // against 6.1, 512 7.7 against 8.4, 1024 11.9 against 12.1; 4096 values: 512 5.0 against 4.9, 1024 8.6
+  // against 8.2).
   const int pieces = (a.K + 511) / 512;        // of 512 values, a wave's worth
   if (pieces <= 1) return launch_forward<BF16, 1, 1>(a, stream);
   if (pieces <= 4) return launch_forward<BF16, 4, 1>(a, stream);
@@ -262,7 +271,8 @@ void backward_for(const NormArgs& a, int grid, hipStream_t stream) {
 
 }  // namespace
 
-// Two workgroups a CU; of few rows one a CU, and a row each at least.
+// Two workgroups a CU; of few rows one a CU, and a row each at least: the second kernel reads a row
+// of sums for each (517 x 2048: 5.7 + 3.3 us, with a workgroup a row 6.4 + 11.4).
 int norm_backward_grid(int64_t T) {
   const int64_t most = T / 4 > 256 ? T / 4 : 256;
   return (int)(T < most ? T : most < kNormMaxGrid ? most : kNormMaxGrid);

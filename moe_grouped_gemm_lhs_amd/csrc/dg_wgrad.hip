@@ -13,7 +13,10 @@
 //
 // What bounds it: the matrix pipe at the clock that the power leaves it; conversions (two
 // instructions for a scaled code, half a one for the others, P's once for each of two waves, Q's
-// for each of four) run beside it.
+// for each of four) run beside it.  16384 rows of 8 groups by (4096, 7168): 1037 us, 0.91 PFLOP/s of
+// the rows that count (a library's bf16 product of 8192^3: 1.31); without the conversions 916 us,
+// without the copies 971, without the stores 1001, without the products 713 (of 1097 then).
+// 1093 rows by (7168, 2048): 42 us, 0.77 PFLOP/s, 11 us of them the fp32 gradient's way to memory.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -480,15 +483,19 @@ void launch(const WgradArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-// Tiles of 256 x 256 (a code is converted for 4 or 2 waves' products of 64 x 128) where they keep
-// half the GPU busy, else of 128 x 128; and of few tiles each group's rows are dealt out among
-// workgroups until the GPU has one a CU, eight blocks of 128 rows each at least if they are one
-// group's.
+// Tiles of 256 x 256 (a code is converted for 4 or 2 waves' products of 64 x 128) where there are
+// more than 128 of them, else of 128 x 128, which then all run at once, two a CU: 2048 rows by
+// (4096, 4096), 256 tiles, 76 us against 109; by (4096, 2048), 128 tiles, 58 against 56; by (2048, 2048)
+// 50 against 38.  Of groups one may have most of the rows, whose tiles then go on alone: more
+// than 64 tiles a group, too (8192 rows, half of them one's, of 8 groups (4096, 2048) 173 us against
+// 240, (2048, 2048) 120 against 124, (2048, 1024) 117 against 75).  Of few tiles each group's rows are
+// dealt out among workgroups until the GPU has one a CU, eight blocks of 128 rows each at least if
+// they are one group's: 8192 rows by (256, 256) 24 us, 249 by one workgroup a tile.
 WgradPlan wgrad_plan(int64_t T, int64_t N, int64_t K, int64_t G) {
   WgradPlan p;
-  const int64_t big = (N + 255) / 256 * ((K + 255) / 256) * G;
-  p.big = big >= 128;
-  const int64_t tiles = p.big ? big : (N / kBlockK) * (K / kBlockK) * G;
+  const int64_t big = (N + 255) / 256 * ((K + 255) / 256);
+  p.big = big > 64 && big * G > 128;
+  const int64_t tiles = (p.big ? big : (N / kBlockK) * (K / kBlockK)) * G;
   const int64_t blocks = (T + kBlockK - 1) / kBlockK;
   int64_t s = tiles > 0 ? 256 / tiles : 1;
   if (s > blocks / 8) s = blocks / 8;

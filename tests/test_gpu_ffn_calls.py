@@ -215,3 +215,56 @@ def test_norm_rows_past_a_launch_and_32_bits():
     at = slice(T - 40, T)
     h = whole[3][at]
     assert gx[at].shape == h.shape and gx[at].isfinite().all() and gw.isfinite().all()
+
+
+def wgrad_check(got, p, sp, q, sq, before=None):
+    """A gradient against the sum in 64 bits."""
+    p, q = R.values(p, sp), R.values(q, sq)
+    want, mag = p.t() @ q, p.abs().t() @ q.abs()
+    if before is not None:
+        want, mag = want + before.double(), mag + before.double().abs()
+    # one factor of each product is rounded to bf16 (2^-8, its scales' product before), the sum of
+    # the products to fp32 at each step, the result to its type
+    tol = mag * (2.0 ** -8 * 1.01 + (p.shape[0] + 4) * 2.0 ** -24) + R.HALF[got.dtype] * want.abs() * 1.01
+    assert ((got.double() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("T", [1, 63, 65, 130, 333, 1000])
+def test_wgrad_large_tiles(T, dtype):
+    """Tiles of 256 x 256 that the last columns of both matrices leave half empty."""
+    N, K = 4224, 2432
+    fp, fq = [("e4m3", "e4m3"), ("e5m2", "e4m3"), ("e4m3", "e5m2"), ("e5m2", "e5m2")][T % 4]
+    n = gen(T)
+    ops = (*R.quantise(0.01 * n(T, N) * torch.exp(n(T, 1)), fp), *R.quantise(n(T, K), fq))
+    wgrad_check(dg.dg_wgrad_fp8(*ops, dtype=dtype), *ops)
+    old = 0.01 * n(N, K).to(dtype)
+    wgrad_check(dg.dg_wgrad_fp8(*ops, old.clone(), accumulate=True), *ops, before=old)
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("order,tail", [([0, 1], 0), ([1, 0, 1], 61), ([1], 7)])
+def test_wgrad_large_tiles_of_groups(order, tail, dtype):
+    """The same of groups: one's rows in two places, one without rows, NaN in rows that count
+    nowhere, a last block that ends early."""
+    N, K, G = 2304, 2176, 2
+    n = gen(tail)
+    idx = []
+    for i, g in enumerate(order):
+        rows = [200, 1, 77][i]
+        blocks = -(-rows // 128) * 128
+        idx += [g] * rows + [-1] * (blocks - rows)
+    idx += [0] * tail
+    idx = torch.tensor(idx, dtype=torch.int32, device=DEV)
+    T = idx.numel()
+    p, sp = R.quantise(0.01 * n(T, N) * torch.exp(n(T, 1)))
+    q, sq = R.quantise(n(T, K))
+    p.view(torch.uint8)[idx < 0] = 0x7F
+    sq[idx < 0] = float("nan")
+    got = dg.dg_grouped_wgrad_fp8_contiguous(p, sp, q, sq, idx, G, dtype=dtype)
+    for g in range(G):
+        at = (idx == g).nonzero()[:, 0]
+        if at.numel():
+            wgrad_check(got[g], p[at], sp[at], q[at], sq[at])
+        else:
+            assert (got[g] == 0).all()
