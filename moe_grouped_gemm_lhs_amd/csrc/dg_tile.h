@@ -5,7 +5,7 @@
 // One templated tile body serves the three forms (dense, contiguous-grouped,
 // masked-grouped); the tile scheduler and the epilogue's row predicate differ.
 // For each output tile and each 128-deep K block kb:
-//   1. the e4m3 bytes of A[m0:m0+BM, kb] and B_g[n0:n0+BN, kb], the scales
+//   1. the fp8 bytes of A[m0:m0+BM, kb] and B_g[n0:n0+BN, kb], the scales
 //      sA[m0:m0+BM, kb] and the few sB_g[nb, kb] the tile needs are copied global -> LDS
 //      with direct-to-LDS buffer loads (buffer_load_dwordx4 / _dword ... lds), STAGES blocks
 //      ahead, so that HBM/L2 traffic for later blocks overlaps the math of this one;
@@ -19,6 +19,7 @@
 //      busy while the VALU works and only three partials are alive at a time;
 //   4. after the last K block the accumulator is rounded to bf16 (nearest-even) and
 //      stored, predicated on the rows the form may write.
+// The gated kernels take 1 and the schedule from here and have 2 to 4 of their own.
 //
 // MFMA operand layout.  v_mfma_f32_16x16x128_f8f6f4 takes 32 bytes per lane for each
 // operand: lane l supplies row l%16 of the first operand and column l%16 of the second,
