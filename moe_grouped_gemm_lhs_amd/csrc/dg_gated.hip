@@ -285,15 +285,20 @@ struct SplitPlan {
 template <class C>
 __device__ __forceinline__ SplitPlan split_plan(const GatedArgs& p, int lane) {
   SplitPlan m;
-  int v = !p.masked_m ? (lane == 0 ? p.rows : 0) : lane < p.G ? p.masked_m[lane] : 0;
-  v = v < 0 ? 0 : (v > p.rows ? p.rows : v);
+  int v = p.rows;                // dense: every lane holds the one group
+  if (p.masked_m) {
+    v = lane < p.G ? p.masked_m[lane] : 0;
+    v = v < 0 ? 0 : (v > p.rows ? p.rows : v);
+  }
   m.mm = v;
   m.rt = (v + C::BM - 1) / C::BM;
   int incl = m.rt;
+  if (p.masked_m) {
 #pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const int u = __shfl_up(incl, off, 64);
-    if (lane >= off) incl += u;
+    for (int off = 1; off < 64; off <<= 1) {
+      const int u = __shfl_up(incl, off, 64);
+      if (lane >= off) incl += u;
+    }
   }
   m.incl = incl;
   const int R = __builtin_amdgcn_readlane(incl, 63);
