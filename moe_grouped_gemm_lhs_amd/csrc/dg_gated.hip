@@ -269,8 +269,8 @@ __device__ __forceinline__ void gated_step(uint8_t* __restrict__ next, const uin
 // of each in a slot of its own in the workspace, and a second kernel adds the slots of a tile in
 // their order, forms h and quantises it.  Nothing waits, and nothing in the workspace need be cleared.
 //
-// (2048, 7168): one row 13.5 us and 64 rows 19.8 (whole tiles 84), both launches; of the second 15 in
-// this kernel, for 29 MB of B and 8.4 MB of sums, and 5 in the next.  8 groups of 16 rows 49 us, 4.8
+// (2048, 7168): one row 12.5 us and 64 rows 16.1 (whole tiles 84), both launches, the second for 29 MB
+// of B and 8.4 MB of sums.  8 groups of 16 rows 49 us, 4.8
 // TB/s (47 with the copies alone); 4 groups of 638 rows together 60 (52): copies into LDS, 21 or 22
 // steps of 48 KB a CU, and products overlap no better than that with the 3 stages that LDS holds.
 constexpr int kSplitGrid = 256;
@@ -540,7 +540,10 @@ gated_finish_kernel(GatedArgs p) {
 }
 
 template <int FA, int FB> using Tile = GatedCfg<Cfg<128, 256, 2, 4, 3, false, FA, FB, 4>>;
-template <int FA, int FB> using Split64 = GatedCfg<Cfg<64, 128, 2, 4, 5, true, FA, FB>>;
+// Three stages leave LDS for a second workgroup a CU, so that a call's first copies are under way
+// while the call before ends: 64 rows of (2048, 7168) 18.7 us against 19.6 with five (with weights
+// that no cache holds; two stages 18.8, but 8 groups of 16 rows 60 against 45).
+template <int FA, int FB, bool NT> using Split64 = GatedCfg<Cfg<64, 128, 2, 4, 3, NT, FA, FB>>;
 
 template <int KIND, class C>
 void launch_tiles(GatedArgs& a, int num_cus, hipStream_t stream) {
@@ -564,7 +567,16 @@ void launch_split(GatedArgs& a, int kind, hipStream_t stream) {
 
 template <int FA, int FB>
 void launch_for(GatedArgs& a, int kind, int num_cus, const GatedPlan& plan, hipStream_t stream) {
-  if (plan.bm == 64) return launch_split<Split64<FA, FB>, Split64<0, 0>>(a, kind, stream);
+  // B past the caches, or not: weights of 64 MB at most stay in the last cache where there is
+  // time to, and more than 32 rows leave it (64 rows of (2048, 7168), weights that were used lately
+  // 16.1 us against 18.5, others 18.2 against 18.7; of (4096, 7168) 21.9 against 24.0, 24.4 against
+  // 24.2).  Else B only passes through (one row 12.5 us either way, other weights 14.2 against 15.2;
+  // 8 groups of 16 rows 45 against 49).
+  if (plan.bm == 64) {
+    const bool keep = a.rows > 32 && (int64_t)(kind == kMasked ? a.G : 1) * a.N * a.K <= (64 << 20);
+    return keep ? launch_split<Split64<FA, FB, false>, Split64<0, 0, false>>(a, kind, stream)
+                : launch_split<Split64<FA, FB, true>, Split64<0, 0, false>>(a, kind, stream);
+  }
   if (plan.bm == 128) return launch_split<Tile<FA, FB>, Tile<0, 0>>(a, kind, stream);
   if (kind == kDense)
     launch_tiles<kDense, Tile<FA, FB>>(a, num_cus, stream);
