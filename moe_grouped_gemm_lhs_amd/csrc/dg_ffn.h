@@ -14,6 +14,7 @@ namespace dg {
 // Root-mean-square norm (defined in dg_norm.hip).
 constexpr int64_t kNormMaxK = 65536;
 constexpr int64_t kNormRows = (int64_t)1 << 20;   // rows of a launch
+constexpr int64_t kNormFewRows = 1024;  // backward in one launch
 constexpr int kNormMaxGrid = 512;       // workgroups that keep sums of a weight's gradient
 
 struct NormArgs {

@@ -230,6 +230,105 @@ __global__ void __launch_bounds__(1024) norm_weight_kernel(const float* partial,
   }
 }
 
+// Backward of few rows, in one launch.  The weight's gradient needs no sum over a row, so that
+// workgroups of their own can form it beside the rows': the first `strips` take a strip of columns
+// each (eight lanes of 16 bytes, 128 rows at a time, KEEP of such loads of both matrices in flight),
+// the others 16 / NW rows each, a piece of 8 values a lane.
+template <bool BF16, int NW>
+__global__ void __launch_bounds__(1024)
+norm_backward_few_kernel(NormArgs a, int strips) {
+  constexpr int CPL = BF16 ? 8 : 4, COLS = 8 * CPL, KEEP = 4;
+  __shared__ float part[16 * COLS];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if ((int)blockIdx.x < strips) {
+    const int c = blockIdx.x * COLS + (lane & 7) * CPL;
+    float sum[CPL];
+#pragma unroll
+    for (int e = 0; e < CPL; ++e) sum[e] = 0.0f;
+    for (int64_t r0 = wave * 8 + (lane >> 3); r0 < a.T; r0 += 128 * KEEP) {
+      uint4 y[KEEP], h[KEEP];
+      float rstd[KEEP];
+#pragma unroll
+      for (int k = 0; k < KEEP; ++k) {
+        const int64_t row = r0 + 128 * k;
+        y[k] = h[k] = make_uint4(0, 0, 0, 0);
+        rstd[k] = 0.0f;
+        if (row < a.T) {
+          y[k] = *(const uint4*)((const uint8_t*)a.x + (row * a.ldx + c) * (BF16 ? 2 : 4));
+          h[k] = *(const uint4*)((const uint8_t*)a.r + (row * a.ldr + c) * (BF16 ? 2 : 4));
+          rstd[k] = a.rstd[row];
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < KEEP; ++k) {
+        const uint32_t wy[4] = {y[k].x, y[k].y, y[k].z, y[k].w}, wh[4] = {h[k].x, h[k].y, h[k].z, h[k].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (BF16) {
+            sum[(2 * e) % CPL] = __builtin_fmaf(__uint_as_float(wy[e] << 16) * __uint_as_float(wh[e] << 16), rstd[k],
+                                                sum[(2 * e) % CPL]);
+            sum[(2 * e + 1) % CPL] = __builtin_fmaf(
+                __uint_as_float(wy[e] & 0xFFFF0000u) * __uint_as_float(wh[e] & 0xFFFF0000u), rstd[k],
+                sum[(2 * e + 1) % CPL]);
+          } else {
+            sum[e] = __builtin_fmaf(__uint_as_float(wy[e]) * __uint_as_float(wh[e]), rstd[k], sum[e]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < CPL; ++e) {
+      sum[e] += __shfl_xor(sum[e], 8, 64);
+      sum[e] += __shfl_xor(sum[e], 16, 64);
+      sum[e] += __shfl_xor(sum[e], 32, 64);
+      if (lane < 8) part[wave * COLS + lane * CPL + e] = sum[e];
+    }
+    __syncthreads();
+    if (threadIdx.x < COLS) {
+      float total = part[threadIdx.x];
+#pragma unroll
+      for (int w = 1; w < 16; ++w) total += part[w * COLS + threadIdx.x];
+      a.grad_w[blockIdx.x * COLS + threadIdx.x] = total;
+    }
+    return;
+  }
+  const int sub = wave / NW;                   // of the workgroup's rows
+  const int64_t row = (int64_t)(blockIdx.x - strips) * (16 / NW) + sub;
+  const int c = ((int)threadIdx.x - sub * NW * 64) * 8;
+  const bool on = row < a.T && c < a.K;
+  Eight<BF16> vy, vh, vg;
+  vy.zero();
+  vh.zero();
+  vg.zero();
+  float rstd = 0.0f, w[8];
+  if (on) {
+    vy.load(a.x, row * a.ldx + c);
+    vh.load(a.r, row * a.ldr + c);
+    if (a.grad_h) vg.load(a.grad_h, row * a.ld_gh + c);
+    rstd = a.rstd[row];
+  }
+  load_weight(a, c, w);
+  float y[8], h[8], g[8], sum = 0.0f;
+  vy.get(y);
+  vh.get(h);
+  vg.get(g);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sum = __builtin_fmaf(y[e] * h[e], w[e], sum);
+  sum = wave_sum(sum);
+  if (lane == 0) part[wave] = sum;
+  __syncthreads();
+  sum = part[sub * NW];
+#pragma unroll
+  for (int i = 1; i < NW; ++i) sum += part[sub * NW + i];
+  if (!on) return;
+  const float m = sum / (float)a.K * rstd * rstd;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) y[e] = __builtin_fmaf(rstd, y[e] * w[e] - h[e] * m, g[e]);
+  Eight<BF16> o;
+  o.set(y);
+  o.store(a.h, row * a.ldh + c);
+}
+
 template <bool BF16, int NW, int C>
 void launch_forward(const NormArgs& a, hipStream_t stream) {
   constexpr int rows = NW < 4 ? 4 / NW : 1;
@@ -269,10 +368,27 @@ void backward_for(const NormArgs& a, int grid, hipStream_t stream) {
   return launch_back<BF16, 16, 8>(a, grid, stream);
 }
 
+template <bool BF16, int NW>
+void launch_few(const NormArgs& a, hipStream_t stream) {
+  int strips = a.grad_w ? a.K / (BF16 ? 64 : 32) : 0;
+  const unsigned rows = (unsigned)((a.T + 16 / NW - 1) / (16 / NW));
+  if (strips && a.h == a.x) {                  // in grad_y's place: the strips have to read it first
+    hipLaunchKernelGGL((norm_backward_few_kernel<BF16, NW>), dim3(strips), dim3(1024), 0, stream, a, strips);
+    strips = 0;
+  }
+  hipLaunchKernelGGL((norm_backward_few_kernel<BF16, NW>), dim3(strips + rows), dim3(1024), 0, stream, a, strips);
+}
+template <bool BF16>
+void few_for(const NormArgs& a, hipStream_t stream) {
+  if (a.K <= 2048) return launch_few<BF16, 4>(a, stream);
+  if (a.K <= 4096) return launch_few<BF16, 8>(a, stream);
+  return launch_few<BF16, 16>(a, stream);
+}
+
 }  // namespace
 
 // Two workgroups a CU; of few rows one a CU, and a row each at least: the second kernel reads a row
-// of sums for each (517 x 2048: 5.7 + 3.3 us, with a workgroup a row 6.4 + 11.4).
+// of sums for each (517 x 2048 by these two kernels: 5.7 + 3.3 us, with a workgroup a row 6.4 + 11.4).
 int norm_backward_grid(int64_t T) {
   const int64_t most = T / 4 > 256 ? T / 4 : 256;
   return (int)(T < most ? T : most < kNormMaxGrid ? most : kNormMaxGrid);
@@ -300,6 +416,11 @@ void launch_norm(const NormArgs& args, hipStream_t stream) {
 }
 
 void launch_norm_backward(const NormArgs& a, hipStream_t stream) {
+  // One launch up to 1024 rows: 517 x 2048 fp32 6.6 us against 9.6, 256 x 7168 bf16 6.7 against 11.6,
+  // 1024 x 7168 bf16 15.9 against 16.6, fp32 29.9 against 29.6; 2048 rows 31.6 against 31.7 and 61.7
+  // against 52.6, as the strips read both matrices again.
+  if (a.T > 0 && a.T <= kNormFewRows && a.K <= 8192)
+    return a.bf16 ? few_for<true>(a, stream) : few_for<false>(a, stream);
   const int grid = norm_backward_grid(a.T);
   if (grid > 0) a.bf16 ? backward_for<true>(a, grid, stream) : backward_for<false>(a, grid, stream);
   if (a.grad_w)

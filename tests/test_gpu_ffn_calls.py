@@ -268,3 +268,29 @@ def test_wgrad_large_tiles_of_groups(order, tail, dtype):
             wgrad_check(got[g], p[at], sp[at], q[at], sq[at])
         else:
             assert (got[g] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("T", [1, 127, 128, 129, 513, 1024, 1025])
+@pytest.mark.parametrize("K", [128, 2048, 2176, 4224, 8192, 8320])
+def test_norm_backward_sizes(T, K, dtype):
+    """Rows and widths on both sides of what the backward pass goes by, with rows apart, and in the
+    gradient's own place."""
+    n = gen(T + K)
+    h = torch.zeros(T, K + 8, device=DEV, dtype=dtype)[:, :K]
+    h.copy_(n(T, K))
+    dy, gh, w = n(T, K).to(dtype), n(T, K).to(dtype), 1 + 0.1 * n(K)
+    rstd = dg.dg_rms_norm_fp8(h, w, codes=False, save=True)[4]
+    dx, dw = dg.dg_rms_norm_backward(dy, h, rstd, w, grad_h=gh)
+    H, Y, r = h.double(), dy.double(), rstd.double()[:, None]
+    g = Y * w.double()
+    m = (g * H).sum(1, keepdim=True) / K
+    want, mean_size = r * (g - H * r * r * m) + gh.double(), (g * H).abs().sum(1, keepdim=True) / K
+    size = r * (g.abs() + H.abs() * r * r * mean_size) + gh.double().abs()
+    # the mean's sum of K products has K roundings at most, the rest a few; the result its type's
+    assert ((dx.double() - want).abs() <= (K + 16) * 2.0 ** -24 * size + R.HALF[dtype] * 1.01 * want.abs()).all()
+    terms = Y * H * r
+    assert ((dw.double() - terms.sum(0)).abs() <= (T + 4) * 2.0 ** -24 * terms.abs().sum(0)).all()
+    own = dy.clone()
+    assert same(dg.dg_rms_norm_backward(own, h, rstd, w, grad_h=gh, grad_x=own), (dx, dw))
+    assert same(dg.dg_rms_norm_backward(dy, h, rstd, w, grad_h=gh, grad_weight=False), (dx, None))
