@@ -275,10 +275,16 @@ __device__ __forceinline__ void gated_step(uint8_t* __restrict__ next, const uin
 // steps of 48 KB a CU, and products overlap no better than that with the 3 stages that LDS holds.
 constexpr int kSplitGrid = 256;
 
+//
+// The contiguous form's row tiles are 128-row blocks, a lane's each; all of them are one piece's
+// workgroups side by side, as neighbours mostly have one group's B.
 struct SplitPlan {
-  int mm;                        // this lane's group: rows under masked_m (dense: one group, all rows)
+  int mm;                        // this lane's group: rows under masked_m (dense: one group, all rows;
+                                 // contiguous: a block's rows, if its first names a group)
   int rt;                        // its row tiles
   int incl;                      // row tiles of groups 0 .. lane
+  int lead;                      // contiguous: the block's group
+  int R;                         // row tiles of all
   unsigned L, Q;                 // iterations of a row tile, pieces that they are cut into
   int total;                     // workgroups
 };
@@ -290,10 +296,16 @@ __device__ __forceinline__ SplitPlan split_plan(const GatedArgs& p, int lane) {
     v = lane < p.G ? p.masked_m[lane] : 0;
     v = v < 0 ? 0 : (v > p.rows ? p.rows : v);
   }
+  m.lead = 0;
+  if (p.group_idx) {             // C::BM is 128 and there are 64 blocks at most (gated_plan)
+    const int left = p.rows - lane * kAlignM;
+    m.lead = left > 0 ? p.group_idx[lane * kAlignM] : -1;
+    v = m.lead < 0 || m.lead >= p.G ? 0 : min(left, kAlignM);
+  }
   m.mm = v;
   m.rt = (v + C::BM - 1) / C::BM;
   int incl = m.rt;
-  if (p.masked_m) {
+  if (p.masked_m || p.group_idx) {
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
       const int u = __shfl_up(incl, off, 64);
@@ -302,6 +314,7 @@ __device__ __forceinline__ SplitPlan split_plan(const GatedArgs& p, int lane) {
   }
   m.incl = incl;
   const int R = __builtin_amdgcn_readlane(incl, 63);
+  m.R = R;
   // pieces of four iterations at least (one costs its first copies' way to memory and the second
   // kernel's reading of its slot), but no longer than a tile
   m.L = (unsigned)p.tiles_n * p.nkb;
@@ -325,11 +338,20 @@ gated_split_kernel(GatedArgs p) {
   // consecutive ones on one XCD (workgroups go round them)
   const unsigned each = (mp.total + 7) / 8, s = (blockIdx.x & 7) * each + (blockIdx.x >> 3);
   if ((blockIdx.x >> 3) >= each || s >= (unsigned)mp.total) return;
-  const int g = (int)__builtin_popcountll(__builtin_amdgcn_ballot_w64(mp.incl * (int)mp.Q <= (int)s));
-  const int rt = __builtin_amdgcn_readlane(mp.rt, g), mm = __builtin_amdgcn_readlane(mp.mm, g);
-  const unsigned o = s - (__builtin_amdgcn_readlane(mp.incl, g) - rt) * mp.Q;
-  const unsigned j = o / (unsigned)rt;
-  const int row0 = (int)(o - j * rt) * C::BM;
+  int g, row0 = 0;
+  unsigned j;
+  if (p.group_idx) {
+    j = s / (unsigned)mp.R;
+    g = (int)__builtin_popcountll(__builtin_amdgcn_ballot_w64(mp.incl <= (int)(s - j * mp.R)));
+  } else {
+    g = (int)__builtin_popcountll(__builtin_amdgcn_ballot_w64(mp.incl * (int)mp.Q <= (int)s));
+    const int rt = __builtin_amdgcn_readlane(mp.rt, g);
+    const unsigned o = s - (__builtin_amdgcn_readlane(mp.incl, g) - rt) * mp.Q;
+    j = o / (unsigned)rt;
+    row0 = (int)(o - j * rt) * C::BM;
+  }
+  const int mm = __builtin_amdgcn_readlane(mp.mm, g);
+  const int bg = p.group_idx ? __builtin_amdgcn_readlane(mp.lead, g) : g;       // B's group
   const unsigned i_begin = piece_start(mp, j), i_end = piece_start(mp, j + 1);
   const int t_first = (int)(i_begin / (unsigned)nkb);
 
@@ -348,10 +370,10 @@ gated_split_kernel(GatedArgs p) {
   cn.wn = wave - cn.wm * C::WAVES_N;
   cn.q = lane >> 4;
   cn.l16 = lane & 15;
-  cn.a_row0 = g * p.rows + row0;
+  cn.a_row0 = g * (p.group_idx ? kAlignM : p.rows) + row0;
   cn.rows = min(C::BM, mm - row0);
-  cn.Bg = p.B + (size_t)g * p.N * p.K;
-  cn.sBg = p.sB + (size_t)g * p.nnb * nkb;
+  cn.Bg = p.B + (size_t)bg * p.N * p.K;
+  cn.sBg = p.sB + (size_t)bg * p.nnb * nkb;
   auto tile = [](TileCtx& c, int t) {
     c.n0 = t * C::BN;
     c.nb_first = c.n0 / (2 * kBlockK);
@@ -430,7 +452,8 @@ gated_finish_kernel(GatedArgs p) {
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int l16 = lane & 15, odd = (lane >> 4) & 1, half = lane >> 5;
   const int nkb = p.nkb, N = p.N >> 1, nb = N / kBlockK;
-  const int groups = (p.rows + C::BM - 1) / C::BM * F::GROUPS;      // of 16 rows, of the capacity
+  const int cap = p.group_idx ? kAlignM : p.rows;      // rows from one group to the next
+  const int groups = (cap + C::BM - 1) / C::BM * F::GROUPS;         // of 16 rows, of the capacity
   const int block = blockIdx.x % (unsigned)nb, r16 = blockIdx.x / (unsigned)nb;
   const int grp = r16 / groups, row0 = (r16 - grp * groups) * 16;
   const SplitPlan mp = split_plan<C>(p, lane);
@@ -439,14 +462,22 @@ gated_finish_kernel(GatedArgs p) {
   const int tn = block * F::TILES + wave / 4, wn = wave % 4;
   const unsigned x0 = (unsigned)tn * nkb, x1 = x0 + nkb - 1;
   const int jf = (int)(((x0 + 1) * mp.Q + mp.L - 1) / mp.L) - 1, jl = (int)(((x1 + 1) * mp.Q + mp.L - 1) / mp.L) - 1;
-  const int n = jl - jf + 1, rt = __builtin_amdgcn_readlane(mp.rt, grp);
-  const int slot = (__builtin_amdgcn_readlane(mp.incl, grp) - rt) * (int)mp.Q + jf * rt + row0 / C::BM;
+  const int n = jl - jf + 1;
+  int rt = __builtin_amdgcn_readlane(mp.rt, grp), slot = __builtin_amdgcn_readlane(mp.incl, grp) - rt;
+  if (p.group_idx) {
+    rt = mp.R;                                         // all row tiles are one piece's
+    slot += jf * rt;
+  } else {
+    slot = slot * (int)mp.Q + jf * rt + row0 / C::BM;
+  }
   const int next = 2 * rt * C::BM * C::BN;             // the row tile's next piece
   // only the first piece can begin before the tile, which is then its second
   const bool second = piece_start(mp, jf) < x0;
   const int in = row0 % C::BM / 32;                    // the 32-row block of the tile
   const int wm = in / (C::WM / 32), I = in % (C::WM / 32);
-  const bool live = row0 + l16 < mm;
+  const int lead = __builtin_amdgcn_readlane(mp.lead, grp);
+  bool live = row0 + l16 < mm;
+  if (live && p.group_idx) live = p.group_idx[grp * kAlignM + row0 + l16] == lead;
   const float* s = p.scratch + (size_t)(slot * 2) * C::BM * C::BN +
                    (size_t)(wm * C::WAVES_N + wn) * C::TI * C::TJ * 256 + (32 * half + row0 % 32 + l16) * 4;
   v4f sum[2][NE];                                      // gate, up; piece e: columns 8 e + 4 half
@@ -507,7 +538,7 @@ gated_finish_kernel(GatedArgs p) {
     if (lane < 16) red[k][wave][l16] = m[k];
   }
   __syncthreads();
-  const size_t row = (size_t)grp * p.rows + row0 + l16;
+  const size_t row = (size_t)grp * cap + row0 + l16;
   const bool store = live && odd == 0;
   // a swap between the lane halves gives a lane consecutive columns: 16 or 8
   const int col = block * kBlockK + wave * C::GW + (C::GW / 2) * half;
@@ -705,11 +736,13 @@ void launch_backward(const GatedBackArgs& a, hipStream_t stream) {
 // (2048, 2048) 28.2 (28.0; whole 29.7), 128 of (12288, 1536) 30.2 (28.7; whole 24.6).  The masked
 // form's counts are not known here: the mean over all of them up to the capacity is taken for
 // them (4 groups of 200 rows, (2048, 4096): 23 to 46 us from a tenth of the rows to all, whole 52 to 55).
+// The contiguous form's blocks are taken as all in use (512 rows of 2 groups, (2048, 7168), 46 us,
+// whole 88; 1024 of 4 74 and 89; 1024 of 4, (2048, 2048), 35 and 33).
 GatedPlan gated_plan(int kind, int64_t rows, int64_t N, int64_t K, int64_t G) {
   GatedPlan p{};
-  if (kind == kContiguous || (kind == kMasked && G > 64)) return p;
+  if ((kind == kContiguous && rows > 64 * kAlignM) || (kind == kMasked && G > 64)) return p;
   const int64_t groups = kind == kMasked ? G : 1;
-  const int bm = rows <= 64 ? 64 : 128, cols = bm == 64 ? 64 : 128;
+  const int bm = rows <= 64 && kind != kContiguous ? 64 : 128, cols = bm == 64 ? 64 : 128;
   if ((rows + bm - 1) / bm * groups * (N / cols) > kSplitGrid) return p;
   // a group's rows and row tiles
   const double full = (double)(rows / bm), rest = (double)(rows % bm);

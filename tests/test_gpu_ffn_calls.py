@@ -294,3 +294,46 @@ def test_norm_backward_sizes(T, K, dtype):
     own = dy.clone()
     assert same(dg.dg_rms_norm_backward(own, h, rstd, w, grad_h=gh, grad_x=own), (dx, dw))
     assert same(dg.dg_rms_norm_backward(dy, h, rstd, w, grad_h=gh, grad_weight=False), (dx, None))
+
+
+# (rows, group) runs; a group's segment starts on a multiple of 128 where the call is to write it
+RUNS = {"one": [(77, 1)], "two": [(128, 0), (100, 2)], "holes": [(5, -1), (123, 0), (130, 2), (126, -1), (128, 7), (60, 0)],
+        "again": [(40, 2), (88, 0), (256, 1), (129, 2)], "none": [(300, -1)],
+        "many": [(256, 0), (200, 1), (56, -1), (384, 2), (128, 1), (300, 0), (20, 3)]}
+
+
+@pytest.mark.parametrize("save", [False, True])
+@pytest.mark.parametrize("K", [1024, 4096])
+@pytest.mark.parametrize("runs", list(RUNS))
+def test_gated_contiguous_few_tiles(runs, K, save):
+    """The contiguous form where its tiles are split: blocks whose first row names no group, rows that
+    do not follow their block's, the same group in several places, out-of-range groups, NaN in
+    every row that is not written."""
+    from tests.test_gpu_gated import check
+    N, G = 256, 3
+    n = gen(K + len(runs))
+    idx = torch.cat([torch.full((r,), g, dtype=torch.int32) for r, g in RUNS[runs]]).to(DEV)
+    T = idx.numel()
+    assert dg.dg_gated_workspace_bytes(dg.DG_CONTIGUOUS, T, N, K, G) > 0 or K < 4096
+    lead = idx[torch.arange(T, device=DEV) // 128 * 128]
+    written = (idx == lead) & (idx >= 0) & (idx < G)
+    a, sa = R.quantise(n(T, K))
+    b, sb = R.quantise_weight(n(G, 2 * N, K) * K ** -0.5)
+    a.view(torch.uint8)[~written] = 0x7F
+    sa[~written] = float("nan")
+    H, GU = (torch.full((T, m), 0x33, dtype=torch.uint8, device=DEV) for m in (N, 2 * N))
+    sH, sGU = torch.full((T, N // 128), -5.0, device=DEV), torch.full((T, N // 64), -5.0, device=DEV)
+    kept = dict(GU=GU, sGU=sGU) if save else {}
+    out = dg.dg_grouped_gated_fp8_contiguous(a, sa, b, sb, idx, H, sH, activation="gelu", **kept)
+    for t, v in ((H, 0x33), (sH, -5)) + (((GU, 0x33), (sGU, -5)) if save else ()):
+        assert (t[~written] == v).all()
+    for g in range(G):
+        at = (written & (idx == g)).nonzero()[:, 0]
+        if at.numel():
+            check(*(o if o is None else o[at] for o in out), R.values(a[at], sa[at]), R.weight_values(b[g], sb[g]),
+                  "gelu", "e4m3", f"group {g}")
+    whole, ws = guarded(dg.dg_gated_workspace_bytes(dg.DG_CONTIGUOUS, T, N, K, G))
+    again = dg.dg_grouped_gated_fp8_contiguous(a, sa, b, sb, idx, H.clone(), sH.clone(), activation="gelu", save=save,
+                                               workspace=ws)
+    assert untouched(whole) and torch.equal(again[0][written].float(), out[0][written].float())
+    assert torch.equal(again[1][written], out[1][written])
