@@ -148,13 +148,14 @@ def test_python_refuses_cpu_tensors(native):
 
 
 def test_gated_workspace_codes(native):
-    """Few tiles need a workspace, many none, the contiguous form never."""
+    """Few tiles need a workspace in every form, many none."""
     need = native.dg_gated_workspace_bytes(0, 64, 2048, 7168, 1)
     assert need > 0
     for bad in (dict(ws=None, wsb=0), dict(wsb=need - 1), dict(ws=A8)):
         assert gated(native, "dense", rows=64, N=2048, K=7168, **bad) == WORKSPACE, bad
     assert native.dg_gated_workspace_bytes(2, 256, 2048, 7168, 4) > 0
     assert native.dg_gated_workspace_bytes(0, 8192, 2048, 7168, 1) == 0
-    assert native.dg_gated_workspace_bytes(1, 200, 2048, 7168, 4) == 0
+    assert native.dg_gated_workspace_bytes(1, 200, 2048, 7168, 4) > 0
+    assert native.dg_gated_workspace_bytes(1, 8192, 2048, 7168, 4) == 0
     assert native.dg_gated_workspace_bytes(0, 64, 100, 7168, 1) == 0
     assert native.dg_gated_workspace_bytes(3, 64, 2048, 7168, 1) == 0
