@@ -10,8 +10,8 @@
 // in a tile (GatedCfg), so that a lane holds g and u of the same elements; each 128-column
 // block of h is one tile's and is quantised from registers.
 //
-// Whole tiles of 128 x 256 (16384 rows of 8 groups, (2048, 7168), with the checkpoint: 874 us, 1.07
-// PFLOP/s of the rows that count): the matrix pipe bounds them at the clock that the power
+// Whole tiles of 128 x 256 (16384 rows of 8 groups, (2048, 7168), with the checkpoint: 846 to
+// 887 us, 1.06 to 1.11 PFLOP/s of the rows that count): the matrix pipe bounds them at the clock that the power
 // leaves it, a step of a K block takes 1.65 us from LDS alone, which is 1.30 PFLOP/s, as a library's
 // bf16 product of 8192^3.  Four waves copy; with all eight 926 us, they wait for their addresses.
 #include <hip/hip_runtime.h>

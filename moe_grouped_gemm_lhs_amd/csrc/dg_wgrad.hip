@@ -13,7 +13,7 @@
 //
 // What bounds it: the matrix pipe at the clock that the power leaves it; conversions (two
 // instructions for a scaled code, half a one for the others, P's once for each of two waves, Q's
-// for each of four) run beside it.  16384 rows of 8 groups by (4096, 7168): 1037 us, 0.91 PFLOP/s of
+// for each of four) run beside it.  16384 rows of 8 groups by (4096, 7168): 1024 to 1060 us, 0.9 PFLOP/s of
 // the rows that count (a library's bf16 product of 8192^3: 1.31); without the conversions 916 us,
 // without the copies 971, without the stores 1001, without the products 713 (of 1097 then).
 // 1093 rows by (7168, 2048): 42 us, 0.77 PFLOP/s, 5 us of them the gradient's way to memory, in bf16.
