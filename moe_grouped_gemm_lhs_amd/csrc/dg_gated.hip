@@ -571,9 +571,9 @@ gated_finish_kernel(GatedArgs p) {
 }
 
 template <int FA, int FB> using Tile = GatedCfg<Cfg<128, 256, 2, 4, 3, false, FA, FB, 4>>;
-// Three stages leave LDS for a second workgroup a CU, so that a call's first copies are under way
-// while the call before ends: 64 rows of (2048, 7168) 18.7 us against 19.6 with five (with weights
-// that no cache holds; two stages 18.8, but 8 groups of 16 rows 60 against 45).
+// Three stages, two of them in flight, are enough: 64 rows of (2048, 7168) 18.7 us against 19.1 with four
+// and 19.6 with five (weights that no cache holds; two stages 18.8, but 8 groups of 16 rows 60
+// against 45).
 template <int FA, int FB, bool NT> using Split64 = GatedCfg<Cfg<64, 128, 2, 4, 3, NT, FA, FB>>;
 
 template <int KIND, class C>
