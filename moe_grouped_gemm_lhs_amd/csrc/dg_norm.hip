@@ -9,8 +9,8 @@
 // between the row's sum and its use.  NW waves share a row and each lane holds C pieces of
 // 8 values, 64 NW 8 apart, so 16 lanes hold one 128-block.
 //
-// Forward, 4096 x 7168 bf16 with a residual: 56 us for 265 MB, 4.7 TB/s (a copy of 256 MB: 5.4); one
-// row 2.8 us, of which an empty launch takes 1.6.  Backward, 8192 x 7168 bf16 with both incoming
+// Forward, 4096 x 7168 bf16 with a residual and bf16 out too: 52 us for 265 MB, 5.1 TB/s (a copy of
+// 256 MB: 5.4); one row 3.0 us, of which an empty launch takes 1.6.  Backward, 8192 x 7168 bf16 with both incoming
 // gradients: 92 us for 470 MB, 5.1 TB/s, and 4.8 for the weight's sums.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -51,6 +51,12 @@ norm_kernel(NormArgs a) {
   const int64_t row = (int64_t)blockIdx.x * ROWS + (ROWS > 1 ? wave : 0);
   if (row >= a.T) return;                      // a wave alone (NW = 1: no barrier below)
   const int t = NW == 1 ? lane : (int)threadIdx.x;
+  constexpr bool KEEP = C <= 2;                // the weights on their way with the row (4096 x 7168 bf16
+  float kept[KEEP ? C : 1][8];                 // 41.3 us against 42.4); longer rows have no registers
+  if (KEEP) {
+#pragma unroll
+    for (int i = 0; i < C; ++i) load_weight(a, (i * NW * 64 + t) * 8, kept[i % (KEEP ? C : 1)]);
+  }
   Eight<BF16> v[C];
   float sum = 0.0f;
   {
@@ -100,7 +106,12 @@ norm_kernel(NormArgs a) {
     if (c >= a.K) continue;                    // whole groups of 16 lanes: K is 128 n
     float x[8], w[8];
     v[i].get(x);
-    load_weight(a, c, w);
+    if constexpr (KEEP) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = kept[i][e];
+    } else {
+      load_weight(a, c, w);
+    }
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = x[e] * rstd * w[e];
     if (a.y) {
@@ -338,15 +349,16 @@ void launch_forward(const NormArgs& a, hipStream_t stream) {
 
 template <bool BF16>
 void forward_for(const NormArgs& a, hipStream_t stream) {
-  // Few rows leave waves idle unless a row has 16 (7168 values: one row 3.1 us against 4.5, 256 rows 4.5
-  // against 6.1, 512 7.7 against 8.4, 1024 11.9 against 12.1; 4096 values: 512 5.0 against 4.9, 1024 8.6
-  // against 8.2).
+  // Eight waves a row from 2048 values on: 4096 x 7168 bf16 42.4 us against 47.4 by four, fp32 72.9
+  // against 78.5, 4096 x 4096 24.7 against 26.7.  Of few rows 16 where each then has a piece: one row
+  // of 7168 3.3 us against 3.5, 256 rows 4.7 against 5.0, 512 7.8 against 7.9, 768 10.0 against 9.6; of
+  // 4096 values 768 rows 7.6 against 6.6.
   const int pieces = (a.K + 511) / 512;        // of 512 values, a wave's worth
   if (pieces <= 1) return launch_forward<BF16, 1, 1>(a, stream);
   if (pieces <= 4) return launch_forward<BF16, 4, 1>(a, stream);
+  if (pieces <= 8) return launch_forward<BF16, 8, 1>(a, stream);
   if (a.T <= 512 && pieces <= 16) return launch_forward<BF16, 16, 1>(a, stream);
-  if (pieces <= 8) return launch_forward<BF16, 4, 2>(a, stream);
-  if (pieces <= 16) return launch_forward<BF16, 4, 4>(a, stream);
+  if (pieces <= 16) return launch_forward<BF16, 8, 2>(a, stream);
   if (pieces <= 32) return launch_forward<BF16, 16, 2>(a, stream);
   if (pieces <= 64) return launch_forward<BF16, 16, 4>(a, stream);
   return launch_forward<BF16, 16, 8>(a, stream);
