@@ -371,10 +371,12 @@ void launch_back(const NormArgs& a, int grid, hipStream_t stream) {
 
 template <bool BF16>
 void backward_for(const NormArgs& a, int grid, hipStream_t stream) {
+  // A piece a lane up to 8192 values: 8192 x 7168 fp32 175 us against 182 with two (bf16 97.8 against
+  // 97.7), 2048 x 4096 fp32 30.4 against 32.3.
   const int pieces = (a.K + 511) / 512;
   if (pieces <= 4) return launch_back<BF16, 4, 1>(a, grid, stream);
-  if (pieces <= 8) return launch_back<BF16, 4, 2>(a, grid, stream);
-  if (pieces <= 16) return launch_back<BF16, 8, 2>(a, grid, stream);
+  if (pieces <= 8) return launch_back<BF16, 8, 1>(a, grid, stream);
+  if (pieces <= 16) return launch_back<BF16, 16, 1>(a, grid, stream);
   if (pieces <= 32) return launch_back<BF16, 16, 2>(a, grid, stream);
   if (pieces <= 64) return launch_back<BF16, 16, 4>(a, grid, stream);
   return launch_back<BF16, 16, 8>(a, grid, stream);
