@@ -337,3 +337,40 @@ def test_gated_contiguous_few_tiles(runs, K, save):
                                                workspace=ws)
     assert untouched(whole) and torch.equal(again[0][written].float(), out[0][written].float())
     assert torch.equal(again[1][written], out[1][written])
+
+
+def test_split_calls_in_a_graph_with_new_rows():
+    """Decode calls whose tiles are split, captured once and replayed with other counts and group
+    indices, all and none of the rows among them, with eager calls between."""
+    n = gen(21)
+    G, cap, T, N, K = 4, 150, 400, 256, 4096
+    b, sb = R.quantise_weight(n(G, 2 * N, K) * K ** -0.5)
+    am, sam = R.quantise(n(G, cap, K))
+    ac, sac = R.quantise(n(T, K))
+    counts = torch.tensor([3, 0, 150, 70], dtype=torch.int32, device=DEV)
+    idx = torch.tensor([0] * 128 + [2] * 200 + [-1] * 72, dtype=torch.int32, device=DEV)
+    assert dg.dg_gated_workspace_bytes(dg.DG_MASKED, cap, N, K, G) > 0
+    assert dg.dg_gated_workspace_bytes(dg.DG_CONTIGUOUS, T, N, K, G) > 0
+
+    def step():
+        m = dg.dg_grouped_gated_fp8_masked(am, sam, b, sb, counts)
+        c = dg.dg_grouped_gated_fp8_contiguous(ac, sac, b, sb, idx, save=True)
+        return [t.view(torch.uint8) if t.element_size() == 1 else t for t in (*m[:2], *c)]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    for c, i in (([150] * 4, [1] * 400), ([0] * 4, [-1] * 400), ([1, 2, 129, 0], [3] * 128 + [3] * 272),
+                 ([-7, 500, 64, 65], [0] * 100 + [-1] * 28 + [9] * 128 + [2] * 144)):
+        counts.copy_(torch.tensor(c, dtype=torch.int32))
+        idx.copy_(torch.tensor(i, dtype=torch.int32))
+        want = step()
+        graph.replay()
+        torch.cuda.synchronize()
+        for p, q in zip(held, want):
+            assert torch.equal(p, q)
