@@ -371,8 +371,8 @@ dg_status dg_rms_norm_fp8(const void *X, int dtype, int64_t ldx, const void *res
  *   g = weight grad_y,  grad_x = rstd (g - h rstd^2 mean(g h)) + grad_h
  *   grad_weight = sum over rows of grad_y h rstd
  * grad_x (dtype) is the gradient by X and by the residual alike; grad_h (dtype, NULL: none) is
- * the gradient that reaches H itself, the residual stream's, and may be grad_x, as grad_y may
- * (same stride).  grad_weight (K fp32, NULL: not wanted) is written, with zeros for T = 0; its
+ * the gradient that reaches H itself, the residual stream's, and may be grad_x, as grad_y and H
+ * may (same stride).  grad_weight (K fp32, NULL: not wanted) is written, with zeros for T = 0; its
  * sums are fp32, in an order that depends on the sizes only.  Shapes and alignments as above.
  * With grad_weight a workspace of dg_rms_norm_backward_workspace_bytes bytes, 16-byte aligned,
  * that may hold anything before and after (see dg_moe_route). */

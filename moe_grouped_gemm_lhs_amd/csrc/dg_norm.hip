@@ -386,7 +386,7 @@ template <bool BF16, int NW>
 void launch_few(const NormArgs& a, hipStream_t stream) {
   int strips = a.grad_w ? a.K / (BF16 ? 64 : 32) : 0;
   const unsigned rows = (unsigned)((a.T + 16 / NW - 1) / (16 / NW));
-  if (strips && a.h == a.x) {                  // in grad_y's place: the strips have to read it first
+  if (strips && (a.h == a.x || a.h == a.r)) {  // in grad_y's or h's place: the strips have to read it first
     hipLaunchKernelGGL((norm_backward_few_kernel<BF16, NW>), dim3(strips), dim3(1024), 0, stream, a, strips);
     strips = 0;
   }

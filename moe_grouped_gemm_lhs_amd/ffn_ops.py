@@ -164,7 +164,7 @@ def dg_rms_norm_backward(grad_y, H, rstd, weight=None, *, grad_h=None, grad_x=No
     """Gradient of dg_rms_norm_fp8 from its H and rstd: grad_y (T x K), the gradient by the
     normalized output, and grad_h (None: none), the gradient that reaches H itself, give
     grad_x, the gradient by X and by the residual alike (all of H's dtype, rows may lie apart;
-    grad_x may be grad_y or grad_h), and, with a weight, grad_weight (K float32).
+    grad_x may be grad_y, grad_h or H), and, with a weight, grad_weight (K float32).
     Returns (grad_x, grad_weight or None); a weight without a gradient: grad_weight=False."""
     native = moe_ops._native or _load_native()
     dev = _device(grad_y, "grad_y")
