@@ -293,13 +293,15 @@ def dg_grouped_gated_fp8_masked(A, sA, B, sB, masked_m, H=None, sH=None, *, acti
                   b_format, fmt, False, None, None, workspace, stream)
 
 
-def dg_gated_backward(grad_H, GU, sGU, D=None, sD=None, *, group_idx=None, groups=1, activation="silu",
+def dg_gated_backward(grad_H, GU, sGU, D=None, sD=None, *, group_idx=None, groups=None, activation="silu",
                       gu_format=None, fmt="e4m3", stream=None):
     """Gradient of the gated block's first half by both projections, from grad_H (T x N float32
     or bfloat16) and the checkpoint GU, sGU: D (T x 2N: by the gate, by up) as fp8 codes of fmt
-    with scales sD (T x 2N/128), which may be GU and sGU.  With group_idx (T int32) and groups
-    rows that the contiguous forward call leaves alone are left alone here (zeros where this
-    call allocates).  Returns (D, sD)."""
+    with scales sD (T x 2N/128), which may be GU and sGU.  With group_idx (T int32) and groups,
+    their number, rows that the contiguous forward call leaves alone are left alone here (zeros
+    where this call allocates).  Returns (D, sD)."""
+    if group_idx is not None and groups is None:
+        raise ValueError("group_idx needs groups, the number of them")
     native = moe_ops._native or _load_native()
     dev = _device(grad_H, "grad_H")
     if _away(dev, stream):
@@ -320,7 +322,8 @@ def dg_gated_backward(grad_H, GU, sGU, D=None, sD=None, *, group_idx=None, group
     sD = _scales_out(sD, (T, 2 * N // 128), dev, zeros)
     p_d = native.vector(D, "D", D.dtype, (T, 2 * N), dev)
     p_sd = native.vector(sD, "sD", torch.float32, (T, 2 * N // 128), dev)
-    st = native.dg_gated_backward(p_g, code, p_gu, gu, p_sgu, p_idx, act, p_d, p_sd, out, T, N, groups,
+    st = native.dg_gated_backward(p_g, code, p_gu, gu, p_sgu, p_idx, act, p_d, p_sd, out, T, N,
+                                  1 if groups is None else groups,
                                   torch._C._cuda_getCurrentRawStream(dev.index))
     if st != 0:
         raise DGError(st, "dg_gated_backward")
