@@ -385,6 +385,8 @@ def dg_grouped_wgrad_fp8_contiguous(P, sP, Q, sQ, group_idx, groups, dW=None, *,
     """dg_wgrad_fp8 for each group of the contiguous form: dW (groups x N x K), of group g the sum
     over the rows that group_idx (T int32) gives it.  Rows of no group count nowhere, whatever
     they hold; a group without rows has a gradient of zeros."""
+    if groups is None:
+        raise TypeError("groups must be a number")
     return _wgrad("dg_grouped_wgrad_fp8_contiguous", P, sP, Q, sQ, group_idx, groups, dW, p_format, q_format,
                   accumulate, dtype, workspace, stream)
 

@@ -16,3 +16,13 @@ def test_gated_backward_asks_for_the_number_of_groups():
     for groups in ({}, dict(groups=3), dict(group_idx=idx, groups=3)):       # the next check's turn
         with pytest.raises(ValueError, match="must be on a GPU"):
             dg.dg_gated_backward(dh, gu, sgu, **groups)
+
+
+def test_weight_gradients_ask_for_the_number_of_groups():
+    """Without it the sum over all rows, whatever their groups, would be returned."""
+    p, sp = torch.zeros(4, 128, dtype=torch.uint8), torch.zeros(4, 1)
+    idx = torch.zeros(4, dtype=torch.int32)
+    with pytest.raises(TypeError, match="groups must be a number"):
+        dg.dg_grouped_wgrad_fp8_contiguous(p, sp, p, sp, idx, None)
+    with pytest.raises(ValueError, match="must be on a GPU"):
+        dg.dg_grouped_wgrad_fp8_contiguous(p, sp, p, sp, idx, 2)
