@@ -358,8 +358,8 @@ dg_status dg_lora_bf16(const uint16_t *X, int64_t ldx, const uint16_t *A, const 
  * Outputs, each NULL if it is not wanted: H (given if and only if residual is; it may be X or
  * residual themselves, with the same stride), codes Q (T x K, dense) with scales S
  * (T x K/128), Y = bf16(y) (its codes come from y, not from Y), rstd (T fp32, for the backward
- * pass).  A row whose h^2 leave the fp32 range has rstd 0; one of zeros needs eps > 0; a row
- * with a NaN is NaN.
+ * pass).  A row whose h^2 pass the fp32 range has rstd 0; one of zeros, or whose h^2 are
+ * below that range, needs eps > 0; a row with a NaN is NaN.
  * 0 < K <= 65536, K % 128 == 0; row strides at least K and multiples of 8 (DG_ERR_SHAPE).
  * X, residual, weight, H, Y 16-byte aligned, Q 8, S and rstd 4. */
 dg_status dg_rms_norm_fp8(const void *X, int dtype, int64_t ldx, const void *residual,

@@ -83,7 +83,7 @@ struct WgradArgs {
   const float* sQ;
   const int32_t* group_idx;    // or nullptr
   void* dW;                    // G x N x K
-  float* partial;              // splits x N x K, or nullptr
+  float* partial;              // splits x G x N x K, or nullptr
   int64_t T;
   int N, K, G;
   int p_fmt, q_fmt, bf16, accumulate;

@@ -25,7 +25,11 @@ namespace dg {
 namespace {
 
 // sigmoid(z(g)), and (DZ) dz/dg.  exp(-z) past fp32's range is infinite or zero, and its
-// sigmoid zero or one.
+// sigmoid zero or one.  exp2 takes the product z log2 e rounded to fp32: the exponential
+// is off by 2^-23 |z| of itself at most, 2^-18.7 at 20, where a sigmoid is 2^-29 or 1.  With the
+// reciprocal's unit of the last place that is 2^-18 or so, against the 2^-4 of half a step of the codes
+// that are made of it, so no instructions go into a second part of the product or a second step of
+// the reciprocal (the VALU bounds the backward pass as much as memory does).
 template <bool DZ>
 __device__ __forceinline__ float act_sigmoid(float g, int act, float* dz) {
   float z = g;

@@ -7,11 +7,14 @@
 //
 // Memory-bound: every value is loaded once, in 16-byte accesses, and stays in registers
 // between the row's sum and its use.  NW waves share a row and each lane holds C pieces of
-// 8 values, 64 NW 8 apart, so 16 lanes hold one 128-block.
+// 8 values, 64 NW 8 apart, so 16 lanes hold one 128-block.  Rows longer than 16384 values
+// (backward) or 32768 (forward, fp32) do not fit the 128 registers that 16 waves leave a lane: the
+// backward pass keeps 200 (C = 4) or 830 (C = 8) bytes a lane in scratch, the forward one 92.
 //
-// Forward, 4096 x 7168 bf16 with a residual and bf16 out too: 52 us for 265 MB, 5.1 TB/s (a copy of
-// 256 MB: 5.4); one row 3.0 us, of which an empty launch takes 1.6.  Backward, 8192 x 7168 bf16 with both incoming
-// gradients: 92 us for 470 MB, 5.1 TB/s, and 4.8 for the weight's sums.
+// Forward, 4096 x 7168 bf16 with a residual and bf16 out too: 51 us for 265 MB, 5.2 TB/s (a copy of
+// 256 MB: 5.4); one row 3.4 us, of which an empty launch takes 1.6; 512 x 65536 62 us, 3.8 TB/s (fp32
+// 128, 3.4).  Backward, 8192 x 7168 bf16 with both incoming gradients: 92 us for 470 MB, 5.1 TB/s,
+// and 4.8 for the weight's sums; 1024 x 32768 129 us, 2.1 TB/s, and 512 x 65536 275, 1.0, out of scratch.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -128,7 +131,8 @@ norm_kernel(NormArgs a) {
 }
 
 // Backward: a workgroup takes rows blockIdx, blockIdx + gridDim, ... and keeps its columns'
-// weights and sums of dy h rstd in registers.  The weights loaded again for each row, four pieces a
+// weights (C <= 2) and sums of dy h rstd in registers (C <= 2; longer rows' partly in scratch).  The
+// weights loaded again for each row, four pieces a
 // lane and 1024 workgroups, whose rows of sums the second kernel reads, took 120 + 21 us of 8192 x
 // 7168, where this takes 92 + 4.8.
 template <bool BF16, int NW, int C>

@@ -444,7 +444,12 @@ def gated_ffn(x, w13, w2, *, residual=None, norm_weight=None, eps=1e-6, activati
     x and residual T x K, the weights, all float32 or bfloat16, are quantised here; what is
     kept for the backward pass is the stream x + residual and codes.
 
+    Between the calls of the backward pass gradients are bfloat16 and E4M3 codes, an fp32 stream's
+    as well: where gradients span more than E4M3's range within 128 columns, the calls themselves
+    take E5M2 ones.
+
     Returns (out T x M bfloat16, x + residual or None without a residual), differentiable once
-    by x, residual, norm_weight, w13 and w2.  A step may be captured in a graph, if no graph of
-    autograd's that was built outside the capture on the same leaves is alive then."""
+    by x, residual, norm_weight, w13 and w2; the backward pass takes M of a multiple of 128.  A
+    step may be captured in a graph, if no graph of autograd's that was built outside the capture
+    on the same leaves is alive then."""
     return _GatedFFN.apply(x, residual, norm_weight, w13, w2, eps, activation)
