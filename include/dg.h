@@ -202,8 +202,8 @@ dg_status dg_grouped_gemm_fp8_masked_ex(const uint8_t *A, int a_format, const fl
  * +-FMAX.  So Q * S reproduces X to within half an fp8 step of each block's scale.
  *
  * Inputs: X rows x K (row-major, DEVICE, 16-byte aligned), x_dtype DG_IN_F32 or
- * DG_IN_BF16; values must be finite (non-finite inputs give unspecified codes and
- * scales, never a fault).  K > 0, K % 128 == 0 (DG_ERR_SHAPE); rows >= 0 (0: nothing
+ * DG_IN_BF16.  A block that holds a NaN has a NaN scale, one that holds an infinity (and no
+ * NaN) an infinite one, and unspecified codes: what uses it comes out infinite or NaN.  K > 0, K % 128 == 0 (DG_ERR_SHAPE); rows >= 0 (0: nothing
  * to do).  Outputs (DEVICE, caller-owned): Q rows x K codes (8-byte aligned); S rows x
  * K/128 (1x128) or ceil(rows/128) x K/128 (128x128) fp32 (4-byte aligned).
  * Errors: DG_ERR_SHAPE, DG_ERR_FORMAT (format or x_dtype), DG_ERR_NULL, DG_ERR_ALIGN,

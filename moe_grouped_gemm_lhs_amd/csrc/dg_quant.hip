@@ -5,7 +5,7 @@
 // Per block (1x128 along a row, or 128x128): amax = max |x| in fp32; scale = amax /
 // FMAX in fp32 (FMAX = 448 for E4M3, 57344 for E5M2; 1 for an all-zero block); each
 // code is x / scale (an IEEE fp32 division) rounded to the nearest fp8 value, ties to
-// even, saturating at +-FMAX.  Inputs are finite fp32 or bf16.  Memory-bound: every
+// even, saturating at +-FMAX.  Inputs are fp32 or bf16.  Memory-bound: every
 // load is 16 bytes (4 fp32 or 8 bf16 inputs) and the matching 4 or 8 codes go out in one
 // store; each lane keeps several loads in flight; the per-element work is three fp32
 // operations for the quotient and the hardware's fp8 conversion.
@@ -47,11 +47,17 @@ __device__ __forceinline__ void expand(const uint4& u, float (&x)[In<BF16>::E]) 
   }
 }
 
+// The larger of two magnitudes, a NaN if either is one: a block that holds a NaN gets a NaN scale (and
+// one that holds an infinity an infinite one), so that no value of it passes for a number.  One
+// instruction for two of them, as the maximum that drops NaNs (four shapes of bf16: 4.15 to 4.19 TB/s,
+// 4.06 to 4.13 with that).
+__device__ __forceinline__ float larger(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
 template <int E>
 __device__ __forceinline__ float amax_of(const float* x) {
   float m = fabsf(x[0]);
 #pragma unroll
-  for (int e = 1; e < E; ++e) m = fmaxf(m, fabsf(x[e]));
+  for (int e = 1; e < E; ++e) m = larger(m, fabsf(x[e]));
   return m;
 }
 
@@ -101,7 +107,7 @@ quant_1x128_kernel(const void* X, uint8_t* Q, float* S, int64_t nblk, int nkb, i
     float amax = amax_of<E>(x[u]);
 #pragma unroll
     for (int off = LPB / 2; off >= 1; off >>= 1)
-      amax = fmaxf(amax, __shfl_xor(amax, off, LPB));
+      amax = larger(amax, __shfl_xor(amax, off, LPB));
     const float scale = amax == 0.0f ? 1.0f : amax / fp8_max<FMT>();
     const float rcp = 1.0f / scale;      // correctly rounded (unused below 2^-64)
     if (b[u] < nblk) {
@@ -149,14 +155,14 @@ quant_128x128_kernel(const void* X, uint8_t* Q, float* S, int64_t rows, int nkb,
     for (int j = 0; j < J; ++j) {
       float x[E];
       expand<BF16>(cur[j], x);
-      amax = fmaxf(amax, amax_of<E>(x));
+      amax = larger(amax, amax_of<E>(x));
     }
 #pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) amax = fmaxf(amax, __shfl_xor(amax, off, 64));
+    for (int off = 32; off >= 1; off >>= 1) amax = larger(amax, __shfl_xor(amax, off, 64));
     if ((t & 63) == 0) wave_max[k & 1][t >> 6] = amax;
     __syncthreads();
-    amax = fmaxf(fmaxf(wave_max[k & 1][0], wave_max[k & 1][1]),
-                 fmaxf(wave_max[k & 1][2], wave_max[k & 1][3]));
+    amax = larger(larger(wave_max[k & 1][0], wave_max[k & 1][1]),
+                  larger(wave_max[k & 1][2], wave_max[k & 1][3]));
     const float scale = amax == 0.0f ? 1.0f : amax / fp8_max<FMT>();
     const float rcp = 1.0f / scale;      // correctly rounded (unused below 2^-64)
     if (t == 0) S[b] = scale;
